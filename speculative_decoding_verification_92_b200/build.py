@@ -1,8 +1,8 @@
 """Build libspecverify.so in-tree with nvcc for sm_100a.
 
 ``python -m speculative_decoding_verification_92_b200.build`` (or
-``build()``) compiles ``csrc/spec_verify.cu`` (which includes the kernel
-headers) and the host-side ``csrc/*.cpp`` into
+``build()``) compiles ``csrc/*.cu`` (which include the kernel headers) and the
+host-side ``csrc/*.cpp`` into
 ``speculative_decoding_verification_92_b200/libspecverify.so``.
 The library is rebuilt only when the sources or the public header change
 (content hash stored beside the library).
@@ -37,9 +37,12 @@ def sources() -> list[Path]:
 
 
 def kernel_sources() -> list[Path]:
-    """The sources the GPU kernels and their launches are built from (the
-    host-only components in csrc/*.cpp and include/sv_host.h excluded)."""
-    return sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + [INCLUDE / "spec_verify.h"]
+    """The sources the GPU kernels of spec_verify and their launches are built
+    from (the host-only components in csrc/*.cpp and include/sv_host.h and the
+    tree operators in csrc/sv_tree* and csrc/sv_cache* excluded)."""
+    own = [p for p in sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh"))
+           if not p.name.startswith(("sv_tree", "sv_cache"))]
+    return own + [INCLUDE / "spec_verify.h"]
 
 
 def kernel_source_hash() -> str:
@@ -95,7 +98,8 @@ def nvcc_command(out: Path, extra=()) -> list[str]:
     return [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared",
             "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
             "-I", str(INCLUDE), "-I", str(CSRC), *extra,
-            "-o", str(out), str(CSRC / "spec_verify.cu"), *[str(p) for p in sorted(CSRC.glob("*.cpp"))]]
+            "--threads", "0", "-o", str(out), *[str(p) for p in sorted(CSRC.glob("*.cu"))],
+            *[str(p) for p in sorted(CSRC.glob("*.cpp"))]]
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), out: Path | None = None) -> Path:
