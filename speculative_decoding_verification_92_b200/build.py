@@ -39,9 +39,9 @@ def sources() -> list[Path]:
 def kernel_sources() -> list[Path]:
     """The sources the GPU kernels of spec_verify and their launches are built
     from (the host-only components in csrc/*.cpp and include/sv_host.h and the
-    tree operators in csrc/sv_tree* and csrc/sv_cache* excluded)."""
+    tree operators in csrc/sv_tree*, sv_cache* and sv_tcgen05* excluded)."""
     own = [p for p in sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh"))
-           if not p.name.startswith(("sv_tree", "sv_cache"))]
+           if not p.name.startswith(("sv_tree", "sv_cache", "sv_tcgen05"))]
     return own + [INCLUDE / "spec_verify.h"]
 
 

@@ -1,0 +1,677 @@
+// sv_tree_attend.cuh -- the attention kernel of sv_tree_attention on the
+// tensor cores, and the kernel that joins what several CTAs found.
+//
+// Mathematics.  For one request and key/value head, the rows of Q are its
+// (node, query head of the group) pairs, up to 256 per unit of work, in tiles
+// of 128.  Per tile of 128 cached rows: S = Q K^T, p = 2^(S c - m) with m a
+// running reference of each row (its maximum so far, or up to 2^8 below it),
+// O += P V, l += sum p.  O and l are rescaled only when the maximum rises by
+// more than 2^8 over the reference: p then stays below 2^8, far from
+// overflow, and most tiles need no pass over O.  p is rounded to the cache's
+// type for the second product; l sums the rounded values, so that the weights
+// of a row sum to one exactly as they are applied.
+//
+// Roles (10 warps).  Warps 0-3 and 4-7 are two softmax groups, a thread per
+// row of S (a lane of tensor memory).  Warp 8 loads K and V tiles by TMA, one
+// box per page and 64 columns, into rings of shared memory.  Warp 9 issues
+// the matrix instructions: S from shared memory, O from P in tensor memory
+// (written over S) and V in shared memory.  With more than 128 rows the
+// groups take one tile of rows each; with fewer they take the even and the
+// odd cached tiles of the same rows, and their results are joined at the end,
+// so that one group's exponentials overlap the other's products.
+//
+// Work split.  The cached tiles of all units form one line that is cut into
+// equal runs, one per CTA (one CTA per SM), whatever the lengths of the
+// requests.  A unit that lies in one run is finished there; the parts of
+// one that is cut go to the workspace and are joined by
+// tree_join_kernel in a fixed order.
+//
+// Bound.  Up to about 256 rows per head the cache's bytes: 64 KiB of K and V
+// per tile take an SM's share of HBM some 1.5 us, the two products of 256
+// rows about 1.1 us.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "sv_tcgen05.cuh"
+#include "sv_tree.h"
+#include "sv_tree_common.cuh"
+
+namespace sv {
+
+constexpr int kTile = 128;                      // cached rows per step, and rows of Q per tile
+constexpr int kUnitRows = 2 * kTile;            // rows of Q per unit of work
+constexpr int kMaskWords = SV_MAX_NODES / 32;
+constexpr int kAttendThreads = 320;
+constexpr int kAttendMaxCtas = 160;
+constexpr uint64_t kAttendTimeoutNs = 2000000000ull;
+
+struct AttnParams {
+    char* kc;
+    char* vc;
+    int64_t page_stride, row_stride, head_stride;  // of the cache, in bytes
+    int32_t pages, page_size, heads, head_dim;
+    int32_t B, N, q_heads, max_pages;
+    int64_t table_stride;
+    int64_t qb, qn, qh, kb, kn, kh, vb, vn, vh, ob, on, oh;  // in bytes
+    const char* q;
+    const char* k;
+    const char* v;
+    char* out;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* parents;
+    const int32_t* counts;
+    float scale;
+    int32_t slot_rows;  // rows of a partial result
+    int32_t* rows;      // [B] cached rows lens + count of a request to compute, 0 = none
+    uint32_t* masks;    // [B][N][kMaskWords] ancestors-or-self of each node
+    int32_t* odd;       // [B][N] the node's value row is not finite
+    float2* part_ml;    // [2 CTAs][slot_rows] reference and sum,
+    float4* part_o;     // [2 CTAs][head_dim / 4][slot_rows] and unnormalised result
+};
+
+template <typename T>
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+    static constexpr uint32_t kNan2 = 0x7fc07fc0u, kExp2 = 0x7f807f80u, kType = 1;
+    static constexpr float kShift = 0.f;
+    __device__ static uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static float sum(uint32_t w) { return bf16_lo(w) + bf16_hi(w); }
+};
+template <>
+struct Half<__half> {
+    static constexpr uint32_t kNan2 = 0x7e007e00u, kExp2 = 0x7c007c00u, kType = 0;
+    // weights are kept 2^6 up, so that small ones do not fall among the
+    // subnormals of a type whose least normal is 2^-14 (2^(6 + 8) < 65504)
+    static constexpr float kShift = 6.f;
+    __device__ static uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static float sum(uint32_t w) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return f.x + f.y;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The line of tiles.
+
+__device__ __forceinline__ int groups_of(const AttnParams& a, int count) {
+    return (count * (a.q_heads / a.heads) + kUnitRows - 1) / kUnitRows;
+}
+// Tiles of request b's units.
+__device__ __forceinline__ int64_t tiles_of(const AttnParams& a, int b) {
+    const int rows = a.rows[b];
+    if (rows == 0) return 0;
+    return int64_t((rows + kTile - 1) / kTile) * a.heads * groups_of(a, rows - a.lens[b]);
+}
+// Sums of v over the threads before this one and over all (whole warps).
+template <int kThreads>
+__device__ int64_t scan_block(int64_t v, int64_t* total, int64_t* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+struct Piece {
+    int b, head, row0, rows_q, len, rows;  // rows: cached rows of the request
+    int first, n, tiles;                   // tiles [first, first + n) of the unit's `tiles`
+    bool split;                            // both groups on the same rows of Q
+};
+
+// Walks this CTA's run; every role has its own.
+struct PieceIter {
+    int b, rem;    // request, tile within the request
+    int64_t left;  // tiles left in the run
+    __device__ bool next(const AttnParams& a, Piece& p) {
+        if (left <= 0) return false;
+        int rows;
+        while ((rows = a.rows[b]) == 0) {
+            ++b;
+            rem = 0;
+        }
+        const int len = a.lens[b], g = a.q_heads / a.heads, R = (rows - len) * g;
+        const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
+        const int unit = rem / tiles;
+        p.b = b;
+        p.head = unit / groups;
+        p.row0 = (unit % groups) * kUnitRows;
+        p.rows_q = R - p.row0 < kUnitRows ? R - p.row0 : kUnitRows;
+        p.len = len;
+        p.rows = rows;
+        p.tiles = tiles;
+        p.first = rem - unit * tiles;
+        p.n = tiles - p.first < left ? tiles - p.first : static_cast<int>(left);
+        p.split = p.rows_q <= kTile;
+        rem += p.n;
+        left -= p.n;
+        if (rem == tiles * a.heads * groups) {
+            ++b;
+            rem = 0;
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct AttendSmem {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kKStages = D == 128 ? 3 : 5;
+    static constexpr int kVStages = D == 128 ? 2 : 4;
+    struct Ctrl {
+        uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
+        uint64_t qfull[2], sfull[2], pfull[2], ofull[2];
+        int64_t warp_sums[kAttendThreads / 32];
+        int64_t left;
+        float m1[kTile], l1[kTile];
+        uint32_t odd[2][2][kTile / 32];  // [group][tile parity]: rows of V that are not finite
+        uint32_t tmem;
+        int32_t b0, rem0;
+    };
+    static constexpr size_t bytes() { return 1024 + size_t(2 + kKStages + kVStages) * kTileBytes + sizeof(Ctrl); }
+};
+
+// The 32 mask bits of cached rows a0 .. a0 + 31 of the tree (rows before the
+// tree are seen by all).
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* mask, int a0) {
+    if (a0 <= -32) return 0xffffffffu;
+    if (a0 < 0) return ((1u << -a0) - 1u) | (mask[0] << -a0);
+    const int w = a0 >> 5, s = a0 & 31;
+    if (w >= kMaskWords) return 0u;
+    return __funnelshift_r(mask[w], w + 1 < kMaskWords ? mask[w + 1] : 0u, s);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
+    using S = AttendSmem<D>;
+    using H = Half<T>;
+    constexpr int KS = S::kKStages, VS = S::kVStages, TB = S::kTileBytes;
+    // tensor memory: scores (then weights) of the two groups, then their results
+    auto s_at = [](int t) { return static_cast<uint32_t>(t * kTile); };
+    auto o_at = [](int t) { return static_cast<uint32_t>(2 * kTile + t * D); };
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* qs = base;               // two tiles of Q
+    unsigned char* ks = base + 2 * TB;
+    unsigned char* vs = ks + KS * TB;
+    auto& ctl = *reinterpret_cast<typename S::Ctrl*>(vs + VS * TB);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(&ctl.kfull[i], 1);
+            mbar_init(&ctl.kempty[i], 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(&ctl.vfull[i], 1);
+            mbar_init(&ctl.vempty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&ctl.qfull[t], kTile);
+            mbar_init(&ctl.sfull[t], 1);
+            mbar_init(&ctl.pfull[t], kTile);
+            mbar_init(&ctl.ofull[t], 1);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&vmap);
+    }
+    if (warp == 9) tmem_alloc(&ctl.tmem, 512);
+    if (tid == 0) ctl.left = 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // this CTA's run of tiles
+    {
+        const int each = (a.B + kAttendThreads - 1) / kAttendThreads;
+        const int lo = tid * each < a.B ? tid * each : a.B, hi = lo + each < a.B ? lo + each : a.B;
+        int64_t mine = 0, total;
+        for (int b = lo; b < hi; ++b) mine += tiles_of(a, b);
+        int64_t at = scan_block<kAttendThreads>(mine, &total, ctl.warp_sums);
+        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+        const int64_t start = per * blockIdx.x;
+        if (mine > 0 && at <= start && start < at + mine) {
+            for (int b = lo; b < hi; ++b) {
+                const int64_t n = tiles_of(a, b);
+                if (start < at + n) {
+                    ctl.b0 = b;
+                    ctl.rem0 = static_cast<int>(start - at);
+                    ctl.left = total - start < per ? total - start : per;
+                    break;
+                }
+                at += n;
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    PieceIter it{ctl.b0, ctl.rem0, ctl.left};
+    Piece p{};
+
+    if (warp == 8) {
+        // ---- loads
+        if (lane == 0) {
+            uint32_t kn = 0, vn = 0;  // tiles issued
+            bool ok = true;
+            const int per_tile = kTile / a.page_size;
+            auto load = [&](const CUtensorMap* map, unsigned char* dst, uint64_t* bar, int tile) {
+                const int page0 = tile * per_tile;
+                const int used = (p.rows + a.page_size - 1) / a.page_size - page0;
+                const int n = used < per_tile ? used : per_tile;
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * a.page_size * D * 2));
+                const int32_t* ids = a.table + p.b * a.table_stride + page0;
+                for (int i = 0; i < n; ++i) {
+                    const int id = ids[i];
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_4d(dst + (x / 64) * (kTile * 128) + i * a.page_size * 128, map, x, p.head, 0, id, bar);
+                }
+            };
+            auto load_k = [&](int tile) {
+                const uint32_t s = kn % KS;
+                ok = ok && (kn < KS || mbar_wait_bounded(&ctl.kempty[s], (kn / KS - 1) & 1, kAttendTimeoutNs));
+                if (ok) load(&kmap, ks + s * TB, &ctl.kfull[s], tile);
+                kn += ok;
+            };
+            auto load_v = [&](int tile) {
+                const uint32_t s = vn % VS;
+                ok = ok && (vn < VS || mbar_wait_bounded(&ctl.vempty[s], (vn / VS - 1) & 1, kAttendTimeoutNs));
+                if (ok) load(&vmap, vs + s * TB, &ctl.vfull[s], tile);
+                vn += ok;
+            };
+            while (ok && it.next(a, p)) {
+                load_k(p.first);
+                for (int i = 0; i < p.n; ++i) {
+                    if (i + 1 < p.n) load_k(p.first + i + 1);
+                    load_v(p.first + i);
+                }
+            }
+            // a wait ran out: nothing may be in flight when the CTA ends
+            if (!ok) {
+                for (uint32_t i = kn > KS ? kn - KS : 0; i < kn; ++i)
+                    mbar_wait_bounded(&ctl.kfull[i % KS], (i / KS) & 1, kAttendTimeoutNs);
+                for (uint32_t i = vn > VS ? vn - VS : 0; i < vn; ++i)
+                    mbar_wait_bounded(&ctl.vfull[i % VS], (i / VS) & 1, kAttendTimeoutNs);
+            }
+        }
+    } else if (warp == 9) {
+        // ---- matrix products
+        if (lane == 0) {
+            uint32_t kn = 0, vn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+            bool ok = true;
+            const uint32_t qaddr = smem_u32(qs), kaddr = smem_u32(ks), vaddr = smem_u32(vs);
+            auto wait = [&](uint64_t* bar, uint32_t n) {
+                ok = ok && mbar_wait_bounded(bar, n & 1, kAttendTimeoutNs);
+                if (ok) tcgen05_fence_after();
+            };
+            auto qk = [&](int t, int qtile) {  // S[t] = Q[qtile] K^T, K the tile `kn`
+                const uint32_t k0 = kaddr + (kn % KS) * TB, q0 = qaddr + qtile * TB;
+#pragma unroll
+                for (int x = 0; x < D; x += 16) {
+                    const uint32_t at = (x / 64) * (kTile * 128) + (x % 64) * 2;
+                    mma_ss(tmem + s_at(t), smem_operand(q0 + at, 16, 1024), smem_operand(k0 + at, 16, 1024),
+                           mma_shape(H::kType, kTile, false), x > 0);
+                }
+                tcgen05_commit(&ctl.sfull[t]);
+            };
+            auto pv = [&](int t, bool add) {  // O[t] (+)= P[t] V, V the tile `vn`
+                const uint32_t v0 = vaddr + (vn % VS) * TB;
+#pragma unroll
+                for (int x = 0; x < kTile; x += 16)
+                    mma_ts(tmem + o_at(t), tmem + s_at(t) + x / 2, smem_operand(v0 + x * 128, kTile * 128, 1024),
+                           mma_shape(H::kType, D, true), add || x > 0);
+            };
+            auto k_ready = [&] { wait(&ctl.kfull[kn % KS], kn / KS); };
+            auto k_done = [&] {
+                tcgen05_commit(&ctl.kempty[kn % KS]);
+                ++kn;
+            };
+            while (ok && it.next(a, p)) {
+                wait(&ctl.qfull[0], qn[0]++);
+                if (!p.split) wait(&ctl.qfull[1], qn[1]++);
+                // the first scores
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (p.split ? t < p.n : t == 0) k_ready();
+                    if (!ok || (p.split && t >= p.n)) break;
+                    qk(t, p.split ? 0 : t);
+                    if (p.split || t == 1) k_done();
+                }
+                for (int i = 0; i < p.n && ok; ++i) {
+                    wait(&ctl.vfull[vn % VS], vn / VS);
+                    if (p.split) {
+                        const int t = i & 1;
+                        wait(&ctl.pfull[t], pn[t]++);
+                        if (!ok) break;
+                        pv(t, i >= 2);
+                        tcgen05_commit(&ctl.vempty[vn % VS]);
+                        ++vn;
+                        if (i + 2 >= p.n) tcgen05_commit(&ctl.ofull[t]);
+                        if (i + 2 < p.n) {
+                            k_ready();
+                            if (!ok) break;
+                            qk(t, 0);
+                            k_done();
+                        }
+                    } else {
+                        for (int t = 0; t < 2 && ok; ++t) {
+                            wait(&ctl.pfull[t], pn[t]++);
+                            if (!ok) break;
+                            pv(t, i > 0);
+                            if (t == 1) tcgen05_commit(&ctl.vempty[vn % VS]);
+                            if (i + 1 == p.n) {
+                                tcgen05_commit(&ctl.ofull[t]);
+                            } else {
+                                if (t == 0) k_ready();
+                                if (!ok) break;
+                                qk(t, t);
+                                if (t == 1) k_done();
+                            }
+                        }
+                        ++vn;
+                    }
+                }
+            }
+        }
+    } else {
+        // ---- softmax: group t, row r (a lane of tensor memory)
+        const int t = warp >> 2, r = tid & (kTile - 1);
+        const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21);
+        const int g = a.q_heads / a.heads;
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+        uint32_t sn = 0, on = 0, vn = 0;
+        bool ok = true;
+        while (it.next(a, p)) {
+            const int tile0 = p.split ? 0 : t * kTile;
+            const int rows_here = p.rows_q - tile0;              // valid rows of this group's tile
+            const bool live = (warp & 3) * 32 < rows_here;       // some row of this warp is valid
+            const int row = p.row0 + tile0 + r, node = row / g, h = p.head * g + row % g;
+            const bool valid = r < rows_here;
+            if (t == 0 || !p.split) {
+                // Q into shared memory, 128-byte swizzle; rows past the unit are zero
+                unsigned char* dst = qs + t * TB + r * 128;
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + p.b * a.qb + node * a.qn + h * a.qh);
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    uint4 w{0, 0, 0, 0};
+                    if (valid) {
+                        w = __ldg(src + x);
+                        w.x ^= sign;
+                        w.y ^= sign;
+                        w.z ^= sign;
+                        w.w ^= sign;
+                    }
+                    *reinterpret_cast<uint4*>(dst + (x / 8) * (kTile * 128) + (((x % 8) ^ (r & 7)) * 16)) = w;
+                }
+                fence_async_shared();
+                mbar_arrive(&ctl.qfull[t]);
+            }
+            const uint32_t* mask = a.masks + (int64_t(p.b) * a.N + (valid ? node : 0)) * kMaskWords;
+            float m = -INFINITY, l = 0.f;
+            const int step = p.split ? 2 : 1, from = p.split ? t : 0;
+            bool odd = false;
+            for (int i = from; i < p.n; i += step) {
+                const int pos0 = (p.first + i) * kTile;
+                const bool tail = pos0 + kTile > p.len;          // holds rows of the tree, or past it
+                // V rows that nobody may see become zero before P V reads them: rows past the
+                // request and rows of the tree that are not finite (they make NaN of the nodes
+                // that see them, below)
+                if (tail) {
+                    const int a0 = pos0 + r - p.len;
+                    const bool past = pos0 + r >= p.rows;
+                    const bool bad = !past && a0 >= 0 && a.odd[int64_t(p.b) * a.N + a0] != 0;
+                    const uint32_t bits = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) ctl.odd[t][sn & 1][warp & 3] = bits;
+                    if (t == 0 || p.split) {
+                        const uint32_t n = vn + i;
+                        ok = ok && mbar_wait_bounded(&ctl.vfull[n % VS], (n / VS) & 1, kAttendTimeoutNs);
+                        if (past || bad) {
+                            unsigned char* vrow = vs + (n % VS) * TB + r * 128;
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x)
+                                *reinterpret_cast<uint4*>(vrow + (x / 8) * (kTile * 128) + (x % 8) * 16) = uint4{0, 0, 0, 0};
+                        }
+                        fence_async_shared();
+                    }
+                    named_barrier_sync(1 + t, kTile);            // the group's bits are written
+                }
+                // (after a wait that ran out every barrier is still met, so that no thread waits for good)
+                const int parity = sn & 1;
+                ok = ok && mbar_wait_bounded(&ctl.sfull[t], parity, kAttendTimeoutNs);
+                ++sn;
+                ok = __all_sync(0xffffffffu, ok);
+                tcgen05_fence_after();
+                if (live && ok) {
+                    uint32_t s[128];
+                    tmem_load(s, lanes + s_at(t));
+                    if (tail) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t see = mask_word(mask, pos0 + 32 * w - p.len);
+                            odd |= (see & ctl.odd[t][parity][w]) != 0;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(see >> k & 1u)) s[32 * w + k] = 0xff800000u;
+                        }
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(s[k]));
+                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c - H::kShift;
+                    const bool rise = i == from ? top > m : top > m + 8.f;
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float f = top > m ? ex2_approx(m - top) : 1.f;   // 0 where there was nothing yet
+                        if (top > m) m = top;
+                        if (i != from) {
+                            l *= f;
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 32) {
+                                uint32_t o[32];
+                                tmem_load(o, lanes + o_at(t) + x);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_store(lanes + o_at(t) + x, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;  // a row that sees nothing here: all weights 0
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float x = ex2_approx(fmaf(__uint_as_float(s[64 * half + 2 * k]), c, -ref));
+                            const float y = ex2_approx(fmaf(__uint_as_float(s[64 * half + 2 * k + 1]), c, -ref));
+                            w[k] = H::pack(x, y);
+                            sum[k & 1] += H::sum(w[k]);
+                        }
+                        tmem_store(lanes + s_at(t) + 32 * half, w);
+                    }
+                    l += sum[0] + sum[1];
+                    tmem_wait_st();
+                }
+                tcgen05_fence_before();
+                mbar_arrive(&ctl.pfull[t]);
+            }
+            vn += p.n;
+            if (odd || !ok) l = NAN;
+            const bool any = from < p.n;
+            if (any) ok = ok && mbar_wait_bounded(&ctl.ofull[t], on++ & 1, kAttendTimeoutNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) l = NAN;
+            tcgen05_fence_after();
+            float f0 = 1.f, f1 = 0.f;
+            if (p.split) {
+                // group 0 joins both groups' results
+                if (t == 1) {
+                    ctl.m1[r] = m;
+                    ctl.l1[r] = l;
+                }
+                named_barrier_sync(3, 2 * kTile);
+                if (t == 0) {
+                    const float mo = ctl.m1[r], lo = ctl.l1[r], M = fmaxf(m, mo);
+                    const float ref = M == -INFINITY ? 0.f : M;
+                    f0 = ex2_approx(m - ref);
+                    f1 = ex2_approx(mo - ref);
+                    l = l * f0 + lo * f1;
+                    m = M;
+                }
+            }
+            if (live && (t == 0 || !p.split)) {
+                const bool whole = p.n == p.tiles;
+                const int64_t slot = 2 * int64_t(blockIdx.x) + (p.first == 0);
+                const int slot_row = tile0 + r;
+                const float inv = 1.f / l;
+                char* dst = a.out + p.b * a.ob + node * a.on + h * a.oh;
+                const bool both = p.split && p.n > 1;
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    tmem_load(o, lanes + o_at(t) + x);
+                    if (p.split) {
+                        uint32_t o1[32];
+                        if (both) tmem_load(o1, lanes + o_at(1) + x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float y = __uint_as_float(o[k]) * f0;
+                            if (both) y = fmaf(__uint_as_float(o1[k]), f1, y);
+                            o[k] = __float_as_uint(y);
+                        }
+                    }
+                    if (!valid) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint4 w;
+                            uint32_t* wp = &w.x;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                wp[e] = H::pack(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4*>(dst + (x + k) * 2) = w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            a.part_o[(slot * (D / 4) + (x + k) / 4) * a.slot_rows + slot_row] =
+                                float4{__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
+                                       __uint_as_float(o[k + 3])};
+                    }
+                }
+                if (valid && !whole) a.part_ml[slot * a.slot_rows + slot_row] = float2{m, l};
+            }
+            tcgen05_fence_before();
+            if (p.split) named_barrier_sync(3, 2 * kTile);       // O of group 1 and the exchange are read
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    if (warp == 9) {
+        __syncwarp();
+        tmem_free(tmem, 512);
+    }
+}
+
+// Joins the parts of units that were cut: 32 rows of one unit per CTA, a lane
+// per row, the columns spread over the warps.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParams a, int units, int ctas) {
+    __shared__ int64_t sums[2][kJoinThreads / 32];
+    const int b = blockIdx.x / units, unit = blockIdx.x % units;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    const int rows = a.rows[b];
+    if (rows == 0) return;
+    const int len = a.lens[b], g = a.q_heads / a.heads, R = (rows - len) * g;
+    const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
+    if (unit >= a.heads * groups) return;
+    const int row0 = (unit % groups) * kUnitRows, r = blockIdx.y * 32 + lane;
+    if (row0 + static_cast<int>(blockIdx.y) * 32 >= R) return;
+    int64_t before = 0, all = 0;
+    for (int i = tid; i < a.B; i += kJoinThreads) {
+        const int64_t n = tiles_of(a, i);
+        all += n;
+        if (i < b) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (lane == 0) {
+        sums[0][warp] = before;
+        sums[1][warp] = all;
+    }
+    __syncthreads();
+    before = all = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        before += sums[0][w];
+        all += sums[1][w];
+    }
+    const int64_t per = (all + ctas - 1) / ctas;
+    const int64_t u0 = before + int64_t(unit) * tiles;
+    const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + tiles - 1) / per);
+    if (c0 == c1 || row0 + r >= R || r >= kUnitRows) return;
+    float M = -INFINITY;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * int64_t(c) + (c == c0)) * a.slot_rows + r].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    const int node = (row0 + r) / g, h = (unit / groups) * g + (row0 + r) % g;
+    char* dst = a.out + b * a.ob + node * a.on + h * a.oh;
+    constexpr int kCols = D / 4 / (kJoinThreads / 32);  // float4 columns of a warp
+    float4 o[kCols] = {};
+    float l = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const int64_t slot = 2 * int64_t(c) + (c == c0);
+        const float2 ml = a.part_ml[slot * a.slot_rows + r];
+        const float f = ex2_approx(ml.x - ref);
+        l += ml.y * f;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            const float4 v = a.part_o[(slot * (D / 4) + warp * kCols + k) * a.slot_rows + r];
+            o[k].x = fmaf(v.x, f, o[k].x);
+            o[k].y = fmaf(v.y, f, o[k].y);
+            o[k].z = fmaf(v.z, f, o[k].z);
+            o[k].w = fmaf(v.w, f, o[k].w);
+        }
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+        *reinterpret_cast<uint2*>(dst + (warp * kCols + k) * 8) =
+            uint2{Half<T>::pack(o[k].x * inv, o[k].y * inv), Half<T>::pack(o[k].z * inv, o[k].w * inv)};
+}
+
+}  // namespace sv

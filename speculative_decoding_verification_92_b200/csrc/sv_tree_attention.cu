@@ -2,9 +2,9 @@
 // values go to a paged cache, and every node attends to the cached prefix and
 // to its own ancestors.
 //
-// Two kernels: tree_prepare_kernel checks each request, works out every
-// node's ancestor set and writes the new rows; tree_attend_kernel computes
-// one (request, node, query head) per warp.
+// tree_prepare_kernel checks each request, works out every node's ancestor
+// set and writes the new rows; tree_attend_kernel (sv_tree_attend.cuh) does
+// the attention and tree_join_kernel joins what it had to cut.
 #include <cmath>
 #include <cstdint>
 
@@ -13,50 +13,21 @@
 #include <cuda_runtime.h>
 
 #include "sv_tree.h"
+#include "sv_tree_attend.cuh"
 #include "sv_tree_common.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kMaskWords = SV_MAX_NODES / 32;
 constexpr int kPrepThreads = 256;
 static_assert(kPrepThreads >= SV_MAX_NODES, "one thread per node");
 
-struct AttnParams {
-    char* kc;
-    char* vc;
-    int64_t page_stride, row_stride, head_stride;  // of the cache, in bytes
-    int32_t pages, page_size, heads, head_dim;
-    int32_t B, N, q_heads, max_pages;
-    int64_t table_stride;
-    int64_t qb, qn, qh, kb, kn, kh, vb, vn, vh, ob, on, oh;  // in bytes
-    const char* q;
-    const char* k;
-    const char* v;
-    char* out;
-    const int32_t* table;
-    const int32_t* lens;
-    const int32_t* parents;
-    const int32_t* counts;
-    float scale;
-    int32_t* rows;     // [B] cached rows lens + count of a request to compute, 0 = none
-    uint32_t* masks;   // [B][N][kMaskWords] ancestors-or-self of each node
-};
-
+// Whether one of two packed values is infinite or NaN (all exponent bits set).
 template <typename T>
-struct Half;
-template <>
-struct Half<__nv_bfloat16> {
-    __device__ static float to(__nv_bfloat16 x) { return __bfloat162float(x); }
-    __device__ static __nv_bfloat16 from(float x) { return __float2bfloat16(x); }
-    static constexpr uint32_t kNan2 = 0x7fc07fc0u;
-};
-template <>
-struct Half<__half> {
-    __device__ static float to(__half x) { return __half2float(x); }
-    __device__ static __half from(float x) { return __float2half(x); }
-    static constexpr uint32_t kNan2 = 0x7e007e00u;
-};
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    constexpr uint32_t e = Half<T>::kExp2;
+    return (w & e & 0xffff0000u) == (e & 0xffff0000u) || (w & e & 0xffffu) == (e & 0xffffu);
+}
 
 // Checks request blockIdx.x, finds each node's ancestors by pointer jumping
 // (log2 rounds), and copies its new rows; blockIdx.y shares out the copies.
@@ -116,56 +87,24 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
                 a.masks[(int64_t(b) * N + tid) * kMaskWords + w] = bits[cur][tid][w];
         if (tid == 0) a.rows[b] = count > 0 ? static_cast<int>(rows) : 0;
     }
-    for (int i = blockIdx.y * kPrepThreads + tid; i < 2 * count * words; i += gridDim.y * kPrepThreads) {
-        const bool value = i >= count * words;
-        const int j = value ? i - count * words : i;
-        const int n = j / words, w = (j % words) * 8, h = w / a.head_dim, d = (w % a.head_dim) * 2;
+    // one warp per node
+    const int lane = tid & 31, warps = gridDim.y * (kPrepThreads / 32);
+    for (int n = blockIdx.y * (kPrepThreads / 32) + tid / 32; n < count; n += warps) {
         const int t = len + n;
         const int64_t page = a.table[b * a.table_stride + t / a.page_size];
-        const int64_t to = page * a.page_stride + (t % a.page_size) * a.row_stride + h * a.head_stride + d;
-        const char* from = value ? a.v + b * a.vb + n * a.vn + h * a.vh + d : a.k + b * a.kb + n * a.kn + h * a.kh + d;
-        *reinterpret_cast<uint4*>((value ? a.vc : a.kc) + to) = *reinterpret_cast<const uint4*>(from);
+        const int64_t to = page * a.page_stride + (t % a.page_size) * a.row_stride;
+        bool odd = false;
+        for (int i = lane; i < words; i += 32) {
+            const int w = i * 8, h = w / a.head_dim, d = (w % a.head_dim) * 2;
+            const uint4 k = *reinterpret_cast<const uint4*>(a.k + b * a.kb + n * a.kn + h * a.kh + d);
+            const uint4 v = *reinterpret_cast<const uint4*>(a.v + b * a.vb + n * a.vn + h * a.vh + d);
+            *reinterpret_cast<uint4*>(a.kc + to + h * a.head_stride + d) = k;
+            *reinterpret_cast<uint4*>(a.vc + to + h * a.head_stride + d) = v;
+            odd |= not_finite<T>(v.x) || not_finite<T>(v.y) || not_finite<T>(v.z) || not_finite<T>(v.w);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) a.odd[int64_t(b) * N + n] = odd;
     }
-}
-
-constexpr int kAttendWarps = 8;
-
-// One warp per (request, node, query head), a position at a time; running
-// maximum and sum in 32 bits.
-template <typename T, int D>
-__global__ void __launch_bounds__(kAttendWarps * 32) tree_attend_kernel(const AttnParams a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t(blockIdx.x) * kAttendWarps + (threadIdx.x >> 5);
-    grid_dependency_wait();
-    if (item >= int64_t(a.B) * a.N * a.q_heads) return;
-    const int h = static_cast<int>(item % a.q_heads), n = static_cast<int>(item / a.q_heads % a.N);
-    const int b = static_cast<int>(item / a.q_heads / a.N);
-    const int rows = a.rows[b], len = a.lens[b];
-    if (n >= rows - len || rows == 0) return;
-    const int kvh = h / (a.q_heads / a.heads);
-    const float c = a.scale * kLog2e;
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-    const T* qp = reinterpret_cast<const T*>(a.q + b * a.qb + n * a.qn + h * a.qh) + lane * E;
-    for (int e = 0; e < E; ++e) q[e] = Half<T>::to(qp[e]);
-    const uint32_t* mask = a.masks + (int64_t(b) * a.N + n) * kMaskWords;
-    for (int t = 0; t < rows; ++t) {
-        if (t >= len && !(mask[(t - len) / 32] >> ((t - len) % 32) & 1u)) continue;
-        const int64_t at = int64_t(a.table[b * a.table_stride + t / a.page_size]) * a.page_stride +
-                           (t % a.page_size) * a.row_stride + kvh * a.head_stride;
-        const T* kp = reinterpret_cast<const T*>(a.kc + at) + lane * E;
-        const T* vp = reinterpret_cast<const T*>(a.vc + at) + lane * E;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += q[e] * Half<T>::to(kp[e]);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= c;
-        const float m2 = fmaxf(m, s), f = ex2_approx(m - m2), p = ex2_approx(s - m2);
-        l = l * f + p;
-        m = m2;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * Half<T>::to(vp[e]);
-    }
-    T* op = reinterpret_cast<T*>(a.out + b * a.ob + n * a.on + h * a.oh) + lane * E;
-    for (int e = 0; e < E; ++e) op[e] = Half<T>::from(o[e] / l);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -184,29 +123,85 @@ sv_status attention_ok(const sv_tree_attention_shape* s, const sv_cache* c) {
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return SV_EUNSUPPORTED;
     if (int64_t(s->max_pages) * c->page_size > 0x40000000 || s->B > 0xffff || s->q_heads > 0x4000)
         return SV_EUNSUPPORTED;
+    // tiles of one request, and units of the batch, are counted in 32 bits
+    const int64_t units = int64_t(c->heads) * ((int64_t(s->N) * (s->q_heads / c->heads) + kUnitRows - 1) / kUnitRows);
+    if (units * (int64_t(s->max_pages) * c->page_size / kTile + 1) > 0x7fffffff || units * s->B > 0x7fffffff)
+        return SV_EUNSUPPORTED;
     return SV_OK;
 }
 
-size_t masks_bytes(const sv_tree_attention_shape& s) { return align256(size_t(s.B) * s.N * kMaskWords * 4); }
-size_t workspace_for(const sv_tree_attention_shape& s) { return align256(size_t(s.B) * 4) + masks_bytes(s); }
+// The workspace: what the preparation finds, then the parts of cut units.
+struct AttnWorkspace {
+    size_t rows, masks, odd, ml, o, total;
+    int slot_rows;
+};
+
+AttnWorkspace workspace_layout(const sv_tree_attention_shape& s, const sv_cache& c) {
+    AttnWorkspace w{};
+    const int64_t most = int64_t(s.N) * (s.q_heads / c.heads);
+    w.slot_rows = static_cast<int>(most < kUnitRows ? (most + 31) / 32 * 32 : kUnitRows);
+    const size_t slots = 2 * size_t(kAttendMaxCtas) * w.slot_rows;
+    size_t at = 0;
+    w.rows = at;  at += align256(size_t(s.B) * 4);
+    w.masks = at; at += align256(size_t(s.B) * s.N * kMaskWords * 4);
+    w.odd = at;   at += align256(size_t(s.B) * s.N * 4);
+    w.ml = at;    at += align256(slots * sizeof(float2));
+    w.o = at;     at += align256(slots * c.head_dim * 4);
+    w.total = at;
+    return w;
+}
+
+// A cache as a 4-d tensor (column, head, row of a page, page); a box is the
+// 64 columns of one head in one page, 128-byte swizzled.
+bool cache_map(CUtensorMap* map, void* base, const sv_cache& c) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.heads), cuuint64_t(c.page_size),
+                                cuuint64_t(c.pages)};
+    const cuuint64_t some = cuuint64_t(c.head_dim) * 2;  // the stride of a dimension of size one is not used
+    const cuuint64_t strides[3] = {c.heads > 1 ? cuuint64_t(c.head_stride) * 2 : some,
+                                   c.page_size > 1 ? cuuint64_t(c.row_stride) * 2 : some,
+                                   c.pages > 1 ? cuuint64_t(c.page_stride) * 2 : some};
+    const cuuint32_t box[4] = {64, 1, cuuint32_t(c.page_size), 1}, one[4] = {1, 1, 1, 1};
+    return encode(map, c.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
+                  dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <typename T, int D>
-cudaError_t run(const AttnParams& a, cudaStream_t st) {
-    const int words = a.heads * a.head_dim / 8;
-    const int copies = 2 * a.N * words / (8 * kPrepThreads) + 1;
-    cudaError_t e = launch_dependent(tree_prepare_kernel<T>, dim3(a.B, copies < 32 ? copies : 32), kPrepThreads, 0, 1,
-                                     st, a);
+cudaError_t run(const AttnParams& a, const sv_cache& c, cudaStream_t st) {
+    TreeDevice dev;
+    cudaError_t e = tree_device(&dev);
     if (e != cudaSuccess) return e;
-    const int64_t items = int64_t(a.B) * a.N * a.q_heads;
-    return launch_dependent(tree_attend_kernel<T, D>, dim3(static_cast<unsigned>((items + kAttendWarps - 1) / kAttendWarps)),
-                            kAttendWarps * 32, 0, 1, st, a);
+    CUtensorMap kmap, vmap;
+    if (!cache_map(&kmap, c.k, c) || !cache_map(&vmap, c.v, c)) return cudaErrorInvalidValue;
+    const int splits = (a.N + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+    e = launch_dependent(tree_prepare_kernel<T>, dim3(a.B, splits), kPrepThreads, 0, 1, st, a);
+    if (e != cudaSuccess) return e;
+    auto k = tree_attend_kernel<T, D>;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(AttendSmem<D>::bytes()));
+    if (e != cudaSuccess) return e;
+    const int ctas = dev.sm_count < kAttendMaxCtas ? dev.sm_count : kAttendMaxCtas;
+    e = launch_dependent(k, dim3(ctas), kAttendThreads, AttendSmem<D>::bytes(), 1, st, a, kmap, vmap);
+    if (e != cudaSuccess) return e;
+    const int g = a.q_heads / a.heads, units = a.heads * ((a.N * g + kUnitRows - 1) / kUnitRows);
+    return launch_dependent(tree_join_kernel<T, D>, dim3(static_cast<unsigned>(a.B * units), a.slot_rows / 32),
+                            kJoinThreads, 0, 1, st, a, units, ctas);
 }
 
 }  // namespace
 }  // namespace sv
 
 extern "C" size_t sv_tree_attention_workspace_bytes(const sv_tree_attention_shape* shape, const sv_cache* cache) {
-    return sv::attention_ok(shape, cache) == SV_OK ? sv::workspace_for(*shape) : 0;
+    return sv::attention_ok(shape, cache) == SV_OK ? sv::workspace_layout(*shape, *cache).total : 0;
 }
 
 extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const sv_cache* cache, const void* q,
@@ -216,11 +211,13 @@ extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const s
     using namespace sv;
     if (const sv_status why = attention_ok(s, cache); why != SV_OK) return why;
     if (!q || !k || !v || !page_table || !lens || !out || !workspace || !cache->k || !cache->v) return SV_EINVAL;
-    if (!std::isfinite(scale) || workspace_bytes < workspace_for(*s)) return SV_EINVAL;
+    if (!std::isfinite(scale) || workspace_bytes < workspace_layout(*s, *cache).total) return SV_EINVAL;
     for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(cache->k),
                           static_cast<const void*>(cache->v), static_cast<const void*>(workspace)})
         if (!tree_aligned16(p)) return SV_EINVAL;
     if (s->B == 0) return SV_OK;
+    const AttnWorkspace w = workspace_layout(*s, *cache);
+    char* ws = static_cast<char*>(workspace);
     AttnParams a{static_cast<char*>(cache->k), static_cast<char*>(cache->v), cache->page_stride * 2,
                  cache->row_stride * 2, cache->head_stride * 2, cache->pages, cache->page_size, cache->heads,
                  cache->head_dim, s->B, s->N, s->q_heads, s->max_pages,
@@ -229,13 +226,14 @@ extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const s
                  s->k_stride_h * 2, s->v_stride_b * 2, s->v_stride_n * 2, s->v_stride_h * 2, s->o_stride_b * 2,
                  s->o_stride_n * 2, s->o_stride_h * 2, static_cast<const char*>(q), static_cast<const char*>(k),
                  static_cast<const char*>(v), static_cast<char*>(out), page_table, lens, parents, counts, scale,
-                 static_cast<int32_t*>(workspace),
-                 reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + align256(size_t(s->B) * 4))};
+                 w.slot_rows, reinterpret_cast<int32_t*>(ws + w.rows), reinterpret_cast<uint32_t*>(ws + w.masks),
+                 reinterpret_cast<int32_t*>(ws + w.odd), reinterpret_cast<float2*>(ws + w.ml),
+                 reinterpret_cast<float4*>(ws + w.o)};
     auto st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (cache->dtype == SV_BF16)
-        e = cache->head_dim == 64 ? run<__nv_bfloat16, 64>(a, st) : run<__nv_bfloat16, 128>(a, st);
+        e = cache->head_dim == 64 ? run<__nv_bfloat16, 64>(a, *cache, st) : run<__nv_bfloat16, 128>(a, *cache, st);
     else
-        e = cache->head_dim == 64 ? run<__half, 64>(a, st) : run<__half, 128>(a, st);
+        e = cache->head_dim == 64 ? run<__half, 64>(a, *cache, st) : run<__half, 128>(a, *cache, st);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
