@@ -443,15 +443,20 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             for (int i = from; i < p.n; i += step) {
                 const int pos0 = (p.first + i) * kTile;
                 const bool tail = pos0 + kTile > p.len;          // holds rows of the tree, or past it
+                // (after a wait that ran out every barrier is still met, so that no thread waits for good)
+                const int parity = sn & 1;
+                ok = ok && mbar_wait_bounded(&ctl.sfull[t], parity, kAttendTimeoutNs);
+                ++sn;
                 // V rows that nobody may see become zero before P V reads them: rows past the
                 // request and rows of the tree that are not finite (they make NaN of the nodes
-                // that see them, below)
+                // that see them, below).  The scores of this tile say that the products two tiles back
+                // are done, so the V stage is in this tile's phase or the one before it.
                 if (tail) {
                     const int a0 = pos0 + r - p.len;
                     const bool past = pos0 + r >= p.rows;
                     const bool bad = !past && a0 >= 0 && a.odd[int64_t(p.b) * a.N + a0] != 0;
                     const uint32_t bits = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) ctl.odd[t][sn & 1][warp & 3] = bits;
+                    if (lane == 0) ctl.odd[t][parity][warp & 3] = bits;
                     if (t == 0 || p.split) {
                         const uint32_t n = vn + i;
                         ok = ok && mbar_wait_bounded(&ctl.vfull[n % VS], (n / VS) & 1, kAttendTimeoutNs);
@@ -465,10 +470,6 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     }
                     named_barrier_sync(1 + t, kTile);            // the group's bits are written
                 }
-                // (after a wait that ran out every barrier is still met, so that no thread waits for good)
-                const int parity = sn & 1;
-                ok = ok && mbar_wait_bounded(&ctl.sfull[t], parity, kAttendTimeoutNs);
-                ++sn;
                 ok = __all_sync(0xffffffffu, ok);
                 tcgen05_fence_after();
                 if (live && ok) {
@@ -539,6 +540,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     ctl.l1[r] = l;
                 }
                 named_barrier_sync(3, 2 * kTile);
+                tcgen05_fence_after();
                 if (t == 0) {
                     const float mo = ctl.m1[r], lo = ctl.l1[r], M = fmaxf(m, mo);
                     const float ref = M == -INFINITY ? 0.f : M;
@@ -569,8 +571,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                             o[k] = __float_as_uint(y);
                         }
                     }
-                    if (!valid) continue;
-                    if (whole) {
+                    if (valid && whole) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) {
                             uint4 w;
@@ -580,13 +581,14 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                                 wp[e] = H::pack(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
                             *reinterpret_cast<uint4*>(dst + (x + k) * 2) = w;
                         }
-                    } else {
+                    } else if (valid) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             a.part_o[(slot * (D / 4) + (x + k) / 4) * a.slot_rows + slot_row] =
                                 float4{__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
                                        __uint_as_float(o[k + 3])};
                     }
+                    __syncwarp();
                 }
                 if (valid && !whole) a.part_ml[slot * a.slot_rows + slot_row] = float2{m, l};
             }

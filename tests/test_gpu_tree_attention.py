@@ -119,6 +119,13 @@ def test_long_contexts_and_ragged_batches():
     Case([9000, 3, 0, 4097, 1500], [4, 9, 0, 9, 1], 9, Hkv=2, g=4, page=64, seed=4).check()
 
 
+@pytest.mark.parametrize("N,g,D,page", [(9, 4, 128, 16), (1, 8, 64, 32), (64, 4, 128, 64), (40, 7, 64, 16)])
+def test_runs_of_many_tiles(N, g, D, page):
+    # more tiles than CTAs: every CTA runs through several heads and requests, with short and long last tiles
+    lens = [600 + 37 * i for i in range(40)] + [1, 0, 128, 1790, 1920]
+    Case(lens, [N - (i % 3 == 2) * (N // 2) for i in range(len(lens))], N, Hkv=8, g=g, D=D, page=page, seed=N).check()
+
+
 def test_one_long_request():
     Case([20011], [2], 2, Hkv=1, g=2, page=16, seed=5).check()
 
