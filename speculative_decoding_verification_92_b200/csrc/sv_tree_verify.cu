@@ -16,7 +16,11 @@
 //     sums max(0, p - l q), whatever was rejected before.
 // Why 64 bits: the answer is a whole number.  A vocabulary of 150k tokens has
 // CDF steps of 1e-8 and less; sums in 32 bits move the CDF by more than
-// that, and one draw in some hundred would pick a neighbouring token.
+// that, and one draw in some hundred would pick a neighbouring token.  An
+// acceptance test is another matter: it compares u with a ratio of sums, so a
+// first pass in 32 bits with a proven error bound (kFastError) settles nearly
+// all of them, and only a test within the bound of its border, a rejection or
+// a leaf (which need the exact sums for the draw) makes the pass in 64 bits.
 //
 // Bound.  Only rows on the accepted path are read, so a step is a chain of
 // visits: load latency, the arithmetic of one row, one cluster barrier.  The
@@ -25,6 +29,7 @@
 // contiguous range of the row, which is the unit the final draw looks up.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -37,7 +42,7 @@ namespace {
 constexpr int kTvThreads = 256;
 constexpr int kTvWarps = kTvThreads / 32;
 constexpr int kTvMaxCluster = 16;
-constexpr int kTvUnroll = 4;  // 16-byte loads in flight per lane
+constexpr int kTvCtasPerSm = 4;  // of a large batch; the clusters of a small one have two, with more registers
 
 struct TreeVerifyParams {
     const void* target;
@@ -60,51 +65,86 @@ struct Part {
     int32_t i; // greedy: index of the maximum
 };
 
+// 2^(k/16), its bits less k << 48: adding (16 e + k) << 16 to the upper word
+// then multiplies by 2^e.  Sixteen 64-bit entries lie in 32 banks once, so
+// that no two lanes of a load are ever in conflict.
+constexpr int kExp2Entries = 16;
+__constant__ unsigned long long kExp2Table[kExp2Entries] = {
+    0x3ff0000000000000ull, 0x3fefb5586cf9890full, 0x3fef72b83c7d517bull, 0x3fef387a6e756238ull,
+    0x3fef06fe0a31b715ull, 0x3feedea64c123422ull, 0x3feebfdad5362a27ull, 0x3feeab07dd485429ull,
+    0x3feea09e667f3bcdull, 0x3feea11473eb0187ull, 0x3feeace5422aa0dbull, 0x3feec49182a3f090ull,
+    0x3feee89f995ad3adull, 0x3fef199bdd85529cull, 0x3fef5818dcfba487ull, 0x3fefa4afa2a490daull};
+
+// Relative error of the 32-bit pass.  A weight 2^y has an error of 2^-21 from
+// ex2 and of |y| 2^-22 ln2 from its argument (a rounded difference times a
+// rounded scale): 6e-6 down to y = -30, and what lies lower weighs less than
+// V 2^-30 altogether.  A lane adds at most 400 vectors, 2^-24 each; four
+// joins (batch, lane, warp, CTA) rescale, 6e-6 each.
+constexpr double kFastError = 1e-4;
+constexpr float kFaint = -100.f;  // children below 2^-100 are left to the pass in 64 bits
+
 struct TvShared {
-    double tab[32];                       // 2^(k/32)
-    Part ex[2][kTvMaxCluster][2];         // [parity][rank][target, draft]: what the CTAs tell one another
-    Part warp[2][kTvWarps];               // statistics of the warps' ranges
-    double wres[kTvWarps];                // residual sums of the warps' ranges
-    double cta_p[kTvMaxCluster];          // weight of each CTA: of the row,
-    double cta_r[kTvMaxCluster];          // of the residual
-    double ce[SV_MAX_NODES], cq[SV_MAX_NODES];
-    float cz[SV_MAX_NODES], cy[SV_MAX_NODES];
+    double tab[kExp2Entries];
+    Part ex[2][kTvMaxCluster][2];    // [parity][rank][target, draft]: what the CTAs tell one another
+    Part warp[2][kTvWarps];          // statistics of the warps' ranges
+    double wp[kTvWarps];             // target sums of the warps' ranges, against the CTA's reference
+    double wres[kTvWarps];           // residual sums of the warps' ranges
+    double wscan[kTvWarps];
+    double ce[SV_MAX_NODES], cq[SV_MAX_NODES];                    // the children's weights (draft logits)
+    int32_t child[2][SV_MAX_NODES], ctok[2][SV_MAX_NODES], nchild[2];  // [parity of the level]
     int32_t par[SV_MAX_NODES], tok[SV_MAX_NODES];
-    int32_t child[SV_MAX_NODES], ctok[SV_MAX_NODES];
-    double S[2], wscan[kTvWarps];
-    float M[2], u[SV_MAX_NODES];
-    int32_t nchild, accepted, bad, pick;
+    float u[SV_MAX_NODES];
+    int32_t bad;
 };
 
-// 2^y for y <= 0 or moderately above, relative error about 2^-52: table of
-// 2^(k/32) and a polynomial on |f| <= 1/64 (Tang's table-driven scheme; its
-// remainder (f ln2)^6 / 720 is below 2e-15).  y in [-1000, 1000].
-__device__ __forceinline__ double exp2_table(double y, const double* tab) {
-    const double magic = 6755399441055744.0 / 32.0;  // 1.5 * 2^52 / 32: rounds y to a multiple of 1/32
+// ln2^k / k!, k = 5 .. 1.  From constant memory, where an operation can take
+// them as they are; as literals each would be moved to registers first.
+__constant__ double kExp2Poly[5] = {1.3333558146428443e-3, 9.6181291076284772e-3, 5.5504108664821580e-2,
+                                    2.4022650695910072e-1, 6.9314718055994531e-1};
+
+// 2^y, relative error below 2e-13: table of 2^(k/16) and the Taylor polynomial
+// of degree 5 on |f| <= 1/32 (Tang's table-driven scheme; the remainder is
+// (f ln2)^6 / 720).  A CDF that is off by 2e-13 moves a draw once in some ten
+// million.  y in [-1000, 1000].
+// In two factors: 2^n/16 with its exponent in place, and 2^f near 1 (a sum
+// takes their product in one fused operation).
+__device__ __forceinline__ void exp2_table(double y, const double* tab, double* b, double* q) {
+    const double magic = 6755399441055744.0 / kExp2Entries;  // 1.5 2^52 / 16: rounds y to a multiple of 1/16
     const double t = y + magic;
     const double f = y - (t - magic);
     const int n = __double2loint(t);
-    double p = 1.3333558146428443e-3;                // ln2^k / k!, k = 5 .. 1
-    p = fma(p, f, 9.6181291076284772e-3);
-    p = fma(p, f, 5.5504108664821580e-2);
-    p = fma(p, f, 2.4022650695910072e-1);
-    p = fma(p, f, 6.9314718055994531e-1);
-    const double b = tab[n & 31];
-    const double r = fma(b * f, p, b);
-    return __hiloint2double(__double2hiint(r) + ((n >> 5) << 20), __double2loint(r));
+    double p = kExp2Poly[0];
+    p = fma(p, f, kExp2Poly[1]);
+    p = fma(p, f, kExp2Poly[2]);
+    p = fma(p, f, kExp2Poly[3]);
+    p = fma(p, f, kExp2Poly[4]);
+    *q = fma(p, f, 1.0);
+    const double x = tab[n & (kExp2Entries - 1)];
+    *b = __hiloint2double(__double2hiint(x) + (n << 16), __double2loint(x));
 }
 
 // Weight of z against the reference m: 0 where z is far below (or -inf).
-__device__ __forceinline__ double weight(float z, float m, double c, float cf, const double* tab) {
-    const double y = (static_cast<double>(z) - static_cast<double>(m)) * c;
-    const double w = exp2_table(y, tab);
-    return (z - m) * cf > -900.f ? w : 0.0;
+__device__ __forceinline__ double bulk_weight(float z, float m, double c, float cf, const double* tab) {
+    double b, q;
+    exp2_table((static_cast<double>(z) - static_cast<double>(m)) * c, tab, &b, &q);
+    return (z - m) * cf > -900.f ? b * q : 0.0;
+}
+// The same, not inlined: what runs once or twice per level waits for its
+// instructions to be fetched more than for its arithmetic.
+__device__ __noinline__ double weight(float z, float m, double c, float cf, const double* tab) {
+    return bulk_weight(z, m, c, cf, tab);
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
+__device__ __noinline__ double warp_sum(double v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+// s, held against the reference m, against the reference M >= m.
+template <bool kExact>
+__device__ __forceinline__ double rescale(double s, float m, float M, double c, float cf, const double* tab) {
+    if (m == M) return s;  // also where both are -inf (s = 0)
+    if (m == -INFINITY) return 0.0;
+    return s * (kExact ? weight(m, M, c, cf, tab) : static_cast<double>(ex2_approx((m - M) * cf)));
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -112,106 +152,180 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// One batch of a warp's range: kTvUnroll vectors per lane from element `base`
-// on, as fp32; elements at or past `hi` are -inf and are not read.  Element
-// j of vector u is element index(base, u, lane) + j of the row (kVec), or the
-// lane-interleaved order for rows without 16-byte alignment.
-template <typename T, bool kVec>
+// A warp's range of a row, in batches of kUnroll 16-byte vectors per lane,
+// kept as they were stored.  Element e of vector u is element
+// base + u kStep + lane EV + e of the row; those at or past `hi` are -inf and
+// are not loaded.
+template <typename T, bool kVec, int kUnroll>
 struct Batch {
     static constexpr int EV = Logit<T>::kPerVec;
-    static constexpr int kElems = EV * kTvUnroll;      // per lane
-    static constexpr int kStep = 32 * kElems;          // per warp
-    float z[kElems];
+    static constexpr int kStep = 32 * EV;              // elements of a warp's vector
+    uint4 w[kUnroll];
 
-    __device__ __forceinline__ static int index(int base, int k, int lane) {
-        return kVec ? base + (k / EV) * (32 * EV) + lane * EV + k % EV : base + k * 32 + lane;
-    }
-    // Whether vector u of this batch lies (for some lane) before `hi`.
-    __device__ __forceinline__ static bool live(int base, int u, int hi) { return base + u * 32 * EV < hi; }
     __device__ __forceinline__ void load(const void* row, int base, int hi, int lane) {
-        uint4 w[kTvUnroll];
-        const uint4* p = reinterpret_cast<const uint4*>(row) + base / EV + lane;
 #pragma unroll
-        for (int u = 0; u < kTvUnroll; ++u)
-            if (kVec && live(base, u + 1, hi + 1)) w[u] = __ldg(p + u * 32);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int at = base + u * kStep;
+            if (kVec && at + kStep <= hi) w[u] = __ldg(reinterpret_cast<const uint4*>(row) + at / EV + lane);
+            else if (at < hi) w[u] = ragged(row, at + lane * EV, hi);
+            else w[u] = uint4{kEmpty, kEmpty, kEmpty, kEmpty};
+        }
+    }
+    static constexpr uint32_t kEmpty = EV == 4 ? 0xff800000u : 0xff80ff80u;
+    // Elements [i, i + EV) of the row one by one, those from hi on as -inf.
+    __device__ __noinline__ static uint4 ragged(const void* row, int i, int hi) {
+        uint32_t x[4];
 #pragma unroll
-        for (int u = 0; u < kTvUnroll; ++u) {
-            if (kVec && live(base, u + 1, hi + 1)) {
-                float f[EV];
-                Logit<T>::unpack(w[u], f);
-#pragma unroll
-                for (int e = 0; e < EV; ++e) z[u * EV + e] = f[e];
+        for (int k = 0; k < 4; ++k) {
+            const int at = i + k * (EV / 4);
+            if constexpr (EV == 4) {
+                x[k] = at < hi ? __ldg(reinterpret_cast<const uint32_t*>(row) + at) : 0xff800000u;
             } else {
+                const uint32_t lo = at < hi ? __ldg(reinterpret_cast<const unsigned short*>(row) + at) : 0xff80u;
+                const uint32_t up = at + 1 < hi ? __ldg(reinterpret_cast<const unsigned short*>(row) + at + 1) : 0xff80u;
+                x[k] = lo | up << 16;
+            }
+        }
+        return uint4{x[0], x[1], x[2], x[3]};
+    }
+    // Takes the listed tokens out (few, and in few ranges).
+    __device__ __forceinline__ void drop(const int32_t* tok, int n, int base, int lane) {
+        for (int c = 0; c < n; ++c) {
+            const int i = tok[c] - base - lane * EV;   // place behind this lane's first element
+            if (i < 0) continue;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
                 for (int e = 0; e < EV; ++e) {
-                    const int i = index(base, u * EV + e, lane);
-                    z[u * EV + e] = i < hi ? Logit<T>::load(row, i) : -INFINITY;
+                    if (i != u * kStep + e) continue;
+                    if (EV == 4) x[e] = 0xff800000u;
+                    else x[e / 2] = e % 2 ? (x[e / 2] & 0xffffu) | 0xff800000u : (x[e / 2] & 0xffff0000u) | 0xff80u;
                 }
+                w[u] = uint4{x[0], x[1], x[2], x[3]};
             }
         }
     }
-    // Takes the listed tokens out (one of `n` at a time; rare).
-    __device__ __forceinline__ void drop(const int32_t* tok, int n, int base, int lane) {
-        for (int c = 0; c < n; ++c) {
-            const int t = tok[c];
-            if (t < base || t >= base + kStep) continue;
+    __device__ __forceinline__ float top() const {
+        if constexpr (EV == 8) {  // two elements per instruction
+            uint32_t m = w[0].x;
 #pragma unroll
-            for (int k = 0; k < kElems; ++k)
-                if (index(base, k, lane) == t) z[k] = -INFINITY;
+            for (int u = 0; u < kUnroll; ++u)
+                m = bf16x2_max(bf16x2_max(bf16x2_max(w[u].x, w[u].y), bf16x2_max(w[u].z, w[u].w)), m);
+            return fmaxf(bf16_lo(m), bf16_hi(m));
+        } else {
+            float m = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                float f[EV];
+                Logit<T>::unpack(w[u], f);
+                m = fmaxf(m, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+            }
+            return m;
         }
     }
 };
 
 // Statistics of a row's range [lo, hi) without the n listed tokens: reference
-// and sum of the whole warp (every lane has them).
-template <typename T, bool kVec>
-__device__ Part range_stats(const void* row, int lo, int hi, const int32_t* drop, int n, double c, const double* tab) {
-    using B = Batch<T, kVec>;
+// and sum of the whole warp (every lane has them), in 64 bits (kExact) or to
+// kFastError.  m is the reference to start from, the same in every lane, warp
+// and CTA (some logit of the row; -inf: none).  The exponents' range leaves
+// room above it, so it moves only past 2^600 (2^60 in 32 bits): nothing waits
+// for a running maximum, and sums nearly always join without being rescaled.
+template <typename T, bool kVec, bool kExact>
+__device__ __forceinline__ Part range_stats(const void* row, int lo, int hi, const int32_t* drop, int n, float m,
+                                            double c, const double* tab) {
+    constexpr int kUnroll = kExact ? 2 : 4;  // 64 bits are bound by their arithmetic
+    constexpr float kRoom = kExact ? 600.f : 60.f;
+    using Sum = std::conditional_t<kExact, double, float>;
+    using B = Batch<T, kVec, kUnroll>;
     const int lane = threadIdx.x & 31;
     const float cf = static_cast<float>(c);
     bool any = false;
     for (int k = lane; k < n; k += 32) any |= drop[k] >= lo && drop[k] < hi;
     any = __any_sync(0xffffffffu, any);
-    float m = -INFINITY;
-    double s = 0.0;
-    for (int base = lo; base < hi; base += B::kStep) {
+    float ref, least;
+    double md, mc;
+    bool near = false;
+    auto refer = [&] {
+        ref = m == -INFINITY ? 0.f : m;
+        md = static_cast<double>(ref);
+        mc = md * c;
+        near = fabs(mc) < 4096.0;
+        least = fmaxf(ref - 900.f / cf, -3.402823466e38f);  // below 2^-900: nothing
+    };
+    refer();
+    Sum s[2] = {0, 0};
+    for (int base = lo; base < hi; base += kUnroll * B::kStep) {
         B b;
         b.load(row, base, hi, lane);
         if (any) b.drop(drop, n, base, lane);
-        float bm = b.z[0];
-#pragma unroll
-        for (int k = 1; k < B::kElems; ++k) bm = fmaxf(bm, b.z[k]);
-        if (bm > m) {
-            s = m == -INFINITY ? 0.0 : s * weight(m, bm, c, cf, tab);
+        const float bm = b.top();
+        if ((bm - m) * cf > kRoom) {
+            const Sum f = m == -INFINITY ? Sum(0) : Sum(rescale<kExact>(1.0, m, bm, c, cf, tab));
+            s[0] *= f;
+            s[1] *= f;
             m = bm;
+            refer();
         }
-        if (m != -INFINITY) {
 #pragma unroll
-            for (int u = 0; u < kTvUnroll; ++u) {
-                if (!B::live(base, u, hi)) break;
-                double a[2] = {0.0, 0.0};
+        for (int u = 0; u < kUnroll; ++u) {
+            if (base + u * B::kStep >= hi) break;
+            float z[B::EV];
+            Logit<T>::unpack(b.w[u], z);
+            if constexpr (kExact) {
+                // one operation for y where rounding m c (the same for all) is below 2^-41, else two
+                auto add = [&](auto y) {
 #pragma unroll
-                for (int e = 0; e < B::EV; ++e) a[e & 1] += weight(b.z[u * B::EV + e], m, c, cf, tab);
-                s += a[0] + a[1];
+                    for (int k = 0; k < B::EV; ++k) {
+                        double x, q;
+                        exp2_table(y(static_cast<double>(z[k])), tab, &x, &q);
+                        s[k & 1] = fma(z[k] >= least ? x : 0.0, q, s[k & 1]);
+                    }
+                };
+                if (near) add([&](double v) { return fma(v, c, -mc); });
+                else add([&](double v) { return (v - md) * c; });
+            } else {
+                float a[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < B::EV; ++k) a[k & 1] += ex2_approx((z[k] - ref) * cf);
+                s[u & 1] += a[0] + a[1];
             }
         }
     }
-    const float M = warp_max(m);
-    if (m != -INFINITY) s *= weight(m, M, c, cf, tab);
-    return Part{warp_sum(s), M, 0};
+    Sum all = s[0] + s[1];
+    float M = __shfl_sync(0xffffffffu, m, 0);
+    if (!__all_sync(0xffffffffu, m == M)) {
+        M = warp_max(m);
+        all = static_cast<Sum>(rescale<kExact>(all, m, M, c, cf, tab));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    return Part{static_cast<double>(all), M, 0};
 }
 
 // Greedy: maximum and its lowest index.
 template <typename T, bool kVec>
-__device__ Part range_argmax(const void* row, int lo, int hi) {
-    using B = Batch<T, kVec>;
+__device__ __forceinline__ Part range_argmax(const void* row, int lo, int hi) {
+    using B = Batch<T, kVec, 4>;
     const int lane = threadIdx.x & 31;
     VI best{-INFINITY, 0x7fffffff};
-    for (int base = lo; base < hi; base += B::kStep) {
+    for (int base = lo; base < hi; base += 4 * B::kStep) {
         B b;
         b.load(row, base, hi, lane);
+        const float bm = b.top();
+        if (bm > best.v || base == lo) {  // the first place where it stands
+            int at = 0x7fffffff;
 #pragma unroll
-        for (int k = 0; k < B::kElems; ++k) best = vi_better(best, VI{b.z[k], B::index(base, k, lane)});
+            for (int u = 3; u >= 0; --u) {
+                float z[B::EV];
+                Logit<T>::unpack(b.w[u], z);
+#pragma unroll
+                for (int k = B::EV - 1; k >= 0; --k)
+                    if (z[k] == bm) at = base + u * B::kStep + lane * B::EV + k;
+            }
+            best = VI{bm, at};
+        }
     }
     best = warp_merge_vi(best);
     return Part{0.0, best.v, best.i};
@@ -219,9 +333,9 @@ __device__ Part range_argmax(const void* row, int lo, int hi) {
 
 // sum over [lo, hi) of max(0, p - l q)
 template <typename T, bool kVec>
-__device__ double range_residual(const void* zr, const void* yr, int lo, int hi, float Mp, float Mq, double ip,
-                                 double lq, double c, const double* tab) {
-    using B = Batch<T, kVec>;
+__device__ __forceinline__ double range_residual(const void* zr, const void* yr, int lo, int hi, float Mp, float Mq,
+                                                 double ip, double lq, double c, const double* tab) {
+    using B = Batch<T, kVec, 1>;
     const int lane = threadIdx.x & 31;
     const float cf = static_cast<float>(c);
     double s = 0.0;
@@ -229,44 +343,61 @@ __device__ double range_residual(const void* zr, const void* yr, int lo, int hi,
         B a, b;
         a.load(zr, base, hi, lane);
         b.load(yr, base, hi, lane);
+        float z[B::EV], y[B::EV];
+        Logit<T>::unpack(a.w[0], z);
+        Logit<T>::unpack(b.w[0], y);
 #pragma unroll
-        for (int u = 0; u < kTvUnroll; ++u) {
-            if (!B::live(base, u, hi)) break;
-#pragma unroll
-            for (int k = u * B::EV; k < (u + 1) * B::EV; ++k)
-                s += fmax(0.0, weight(a.z[k], Mp, c, cf, tab) * ip - weight(b.z[k], Mq, c, cf, tab) * lq);
-        }
+        for (int k = 0; k < B::EV; ++k)
+            s += fmax(0.0, bulk_weight(z[k], Mp, c, cf, tab) * ip - bulk_weight(y[k], Mq, c, cf, tab) * lq);
     }
     return warp_sum(s);
 }
 
-template <typename T, bool kVec, bool kGreedy>
-__global__ void __launch_bounds__(kTvThreads) tree_verify_kernel(const TreeVerifyParams prm) {
+// The entry that holds `want` when n <= 32 weights (one per lane, 0 beyond)
+// stand in a row: the first whose running sum exceeds it, else the last with
+// weight, -1 when there is none.  *want becomes what is left within it.
+__device__ __noinline__ int pick_entry(double w, int n, double* want, bool* passed = nullptr) {
+    const int lane = threadIdx.x & 31;
+    double incl = w;
+    for (int o = 1; o < n; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, lane < n && w > 0.0);
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < n && w > 0.0 && incl > *want);
+    const int at = hit ? __ffs(hit) - 1 : has ? 31 - __clz(has) : -1;
+    const double before = __shfl_sync(0xffffffffu, incl, at > 0 ? at - 1 : 0);
+    if (at > 0) *want -= before;
+    if (passed) *passed = hit != 0;
+    return at;
+}
+
+// Every CTA of a cluster, and after an exchange every warp of a CTA, takes
+// the same decisions from the same numbers; nothing has to be told twice.
+template <typename T, bool kVec, bool kGreedy, int kCtasPerSm>
+__global__ void __launch_bounds__(kTvThreads, kCtasPerSm) tree_verify_kernel(const TreeVerifyParams prm) {
     __shared__ TvShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_ctarank(), C = cluster_nctarank();
+    const int rank = static_cast<int>(cluster_ctarank()), C = static_cast<int>(cluster_nctarank());
     const int b = blockIdx.x / C;
     const int N = prm.N, V = prm.V;
     const double c = prm.scale;
     const float cf = static_cast<float>(c);
 
-    if (tid < 32) sh.tab[tid] = exp2(tid / 32.0);
+    if (tid < kExp2Entries) sh.tab[tid] = __longlong_as_double(kExp2Table[tid]);
     if (tid == 0) sh.bad = 0;
     cluster_barrier();  // every CTA of the cluster runs before any writes to another's shared memory
     grid_dependency_wait();
     const int count = prm.counts ? prm.counts[b] : N;
-    if (count < 0 || count > N) {
-        if (tid == 0) sh.bad = 1;
-    } else {
-        for (int i = tid; i < count; i += kTvThreads) {
-            const int p = i == 0 ? -1 : prm.parents ? prm.parents[int64_t(b) * N + i] : i - 1;
-            const int t = i == 0 ? 0 : prm.tokens[int64_t(b) * N + i];
-            sh.par[i] = p;
-            sh.tok[i] = t;
-            if (!kGreedy) sh.u[i] = prm.uniforms[int64_t(b) * N + i];
-            if (i > 0 && (p < 0 || p >= i || t < 0 || t >= V)) sh.bad = 1;
-        }
+    for (int i = tid; i < N; i += kTvThreads) {
+        const int p = i == 0 ? -1 : prm.parents ? prm.parents[int64_t(b) * N + i] : i - 1;
+        const int t = i == 0 ? 0 : prm.tokens[int64_t(b) * N + i];
+        sh.par[i] = p;
+        sh.tok[i] = t;
+        if (!kGreedy) sh.u[i] = prm.uniforms[int64_t(b) * N + i];
+        if (i > 0 && i < count && (p < 0 || p >= i || t < 0 || t >= V)) sh.bad = 1;
     }
+    if (tid == 0 && (count < 0 || count > N)) sh.bad = 1;
     __syncthreads();
     int32_t* out_tok = prm.out_tok + int64_t(b) * N;
     int32_t* out_path = prm.out_path + int64_t(b) * N;
@@ -283,37 +414,53 @@ __global__ void __launch_bounds__(kTvThreads) tree_verify_kernel(const TreeVerif
     const int hi = lo + prm.range < V ? lo + prm.range : V;
     int node = 0, j = 0, parity = 0;
 
-    // What each warp found, merged per CTA and told to every CTA.
-    auto exchange = [&](int which) {
-        if (warp == 0 && lane < static_cast<int>(C)) {
-            Part r = sh.warp[which][0];
-            if (kGreedy) {
-                for (int w = 1; w < kTvWarps; ++w) {
-                    const VI v = vi_better(VI{r.m, r.i}, VI{sh.warp[which][w].m, sh.warp[which][w].i});
-                    r.m = v.v;
-                    r.i = v.i;
-                }
-            } else {
-                for (int w = 1; w < kTvWarps; ++w) r.m = fmaxf(r.m, sh.warp[which][w].m);
-                r.s = 0.0;
-                for (int w = 0; w < kTvWarps; ++w)
-                    if (sh.warp[which][w].m != -INFINITY)
-                        r.s += sh.warp[which][w].s * weight(sh.warp[which][w].m, r.m, c, cf, sh.tab);
-            }
+    // One part per lane: their common reference, and the lane's sum against it.
+    auto common = [&](const Part& r, bool exact, float* M) {
+        *M = __shfl_sync(0xffffffffu, r.m, 0);
+        if (__all_sync(0xffffffffu, r.m == *M)) return r.s;
+        *M = warp_max(r.m);
+        return exact ? rescale<true>(r.s, r.m, *M, c, cf, sh.tab) : rescale<false>(r.s, r.m, *M, c, cf, sh.tab);
+    };
+    // What the warps found, merged and told to every CTA: warp 0 the target's
+    // row, warp 1 the draft's.
+    auto exchange = [&](int which, bool exact) {
+        Part r = sh.warp[which][lane % kTvWarps];
+        if (kGreedy) {
+            VI v{r.m, r.i};
+#pragma unroll
+            for (int o = kTvWarps / 2; o > 0; o >>= 1)
+                v = vi_better(v, VI{__shfl_xor_sync(0xffffffffu, v.v, o), __shfl_xor_sync(0xffffffffu, v.i, o)});
+            r = Part{0.0, v.v, v.i};
+        } else {
+            float M;
+            double s = common(r, exact, &M);
+            if (which == 0 && lane < kTvWarps) sh.wp[lane] = s;
+#pragma unroll
+            for (int o = kTvWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            r.s = s;
+            r.m = M;
+        }
+        if (lane < C) {
             Part* at = &sh.ex[parity][rank][which];
             st_cluster_u64(&at->s, lane, __double_as_longlong(r.s));
-            st_cluster_u64(&at->m, lane,
-                           uint64_t(__float_as_uint(r.m)) | uint64_t(static_cast<uint32_t>(r.i)) << 32);
+            st_cluster_u64(&at->m, lane, uint64_t(__float_as_uint(r.m)) | uint64_t(static_cast<uint32_t>(r.i)) << 32);
         }
+    };
+    // The row's reference M and sum; *mine: the weight of CTA lane % C in it.
+    auto row_sum = [&](int which, bool exact, float* M, double* mine) {
+        double s = common(sh.ex[parity][lane & (C - 1)][which], exact, M);
+        *mine = s;
+        for (int o = C >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
     };
 
     for (;;) {
+        const int lv = j & 1;  // the lists of a level live until the next one's are read
         const char* zr = reinterpret_cast<const char*>(prm.target) +
                          (int64_t(b) * N + node) * prm.stride * Logit<T>::kSize;
         const char* yr = reinterpret_cast<const char*>(prm.draft) +
                          (int64_t(b) * N + node) * prm.stride * Logit<T>::kSize;
-        // the node's children, in order
-        if (warp == 0) {
+        if (warp == 0) {  // the node's children, in order
             int n = 0;
             for (int i0 = 0; i0 < count; i0 += 32) {
                 const int i = i0 + lane;
@@ -321,227 +468,205 @@ __global__ void __launch_bounds__(kTvThreads) tree_verify_kernel(const TreeVerif
                 const uint32_t mask = __ballot_sync(0xffffffffu, is);
                 if (is) {
                     const int k = n + __popc(mask & ((1u << lane) - 1u));
-                    sh.child[k] = i;
-                    sh.ctok[k] = sh.tok[i];
+                    sh.child[lv][k] = i;
+                    sh.ctok[lv][k] = sh.tok[i];
                 }
                 n += __popc(mask);
             }
-            if (lane == 0) sh.nchild = n;
+            if (lane == 0) sh.nchild[lv] = n;
         }
         __syncthreads();
-        const int nchild = sh.nchild;
-        const bool use_q = !kGreedy && prm.draft != nullptr && nchild > 0;
-        const bool ids_only = !kGreedy && prm.draft == nullptr;
-        if (kGreedy) {
+        const int nchild = sh.nchild[lv];
+        const int32_t *child = sh.child[lv], *ctok = sh.ctok[lv];
+        int acc = -1;
+        if constexpr (kGreedy) {
             const Part r = range_argmax<T, kVec>(zr, lo, hi);
             if (lane == 0) sh.warp[0][warp] = r;
-        } else {
-            for (int k = tid; k < nchild; k += kTvThreads) {
-                sh.cz[k] = Logit<T>::load(zr, sh.ctok[k]);
-                if (use_q) sh.cy[k] = Logit<T>::load(yr, sh.ctok[k]);
-            }
-            const Part r = range_stats<T, kVec>(zr, lo, hi, sh.ctok, ids_only ? nchild : 0, c, sh.tab);
-            if (lane == 0) sh.warp[0][warp] = r;
-            if (use_q) {
-                const Part q = range_stats<T, kVec>(yr, lo, hi, sh.ctok, 0, c, sh.tab);
-                if (lane == 0) sh.warp[1][warp] = q;
-            }
-        }
-        __syncthreads();
-        exchange(0);
-        if (use_q) exchange(1);
-        cluster_barrier();
-
-        if (kGreedy) {
-            VI g{sh.ex[parity][0][0].m, sh.ex[parity][0][0].i};
-            for (int r = 1; r < static_cast<int>(C); ++r)
-                g = vi_better(g, VI{sh.ex[parity][r][0].m, sh.ex[parity][r][0].i});
-            int next = -1;
-            for (int k = 0; k < nchild && next < 0; ++k)
-                if (sh.ctok[k] == g.i) next = sh.child[k];
+            __syncthreads();
+            if (warp == 0) exchange(0, false);
+            cluster_barrier();
+            VI g{sh.ex[parity][lane & (C - 1)][0].m, sh.ex[parity][lane & (C - 1)][0].i};
+            for (int o = C >> 1; o > 0; o >>= 1)
+                g = vi_better(g, VI{__shfl_xor_sync(0xffffffffu, g.v, o), __shfl_xor_sync(0xffffffffu, g.i, o)});
             parity ^= 1;
-            if (next < 0) {
+            for (int k0 = 0; k0 < nchild && acc < 0; k0 += 32) {
+                const uint32_t hit = __ballot_sync(0xffffffffu, k0 + lane < nchild && ctok[k0 + lane] == g.i);
+                if (hit) acc = k0 + __ffs(hit) - 1;
+            }
+            if (acc < 0) {
                 if (rank == 0 && tid == 0) out_tok[j] = g.i < V ? g.i : 0;
                 break;
             }
-            if (rank == 0 && tid == 0) {
-                out_tok[j] = sh.tok[next];
-                out_path[j + 1] = next;
-            }
-            node = next;
-            ++j;
-            __syncthreads();
-            continue;
-        }
-
-        // row sums, and the children's weights against the row's reference
-        if (warp < (use_q ? 2 : 1)) {
-            Part r{0.0, -INFINITY, 0};
-            if (lane < static_cast<int>(C)) r = sh.ex[parity][lane][warp];
-            float M = r.m;
-            if (warp == 0 && ids_only)
-                for (int k = lane; k < nchild; k += 32) M = fmaxf(M, sh.cz[k]);
-            M = warp_max(M);
-            const double s = r.m == -INFINITY ? 0.0 : r.s * weight(r.m, M, c, cf, sh.tab);
-            if (warp == 0 && lane < kTvMaxCluster) sh.cta_p[lane] = s;
-            const double S = warp_sum(s);
-            if (lane == 0) {
-                sh.M[warp] = M;
-                sh.S[warp] = S;
-            }
-            for (int k = lane; k < nchild; k += 32) {
-                bool again = false;  // an earlier sibling's token: nothing of it is left
-                if (ids_only)
-                    for (int e = 0; e < k; ++e) again |= sh.ctok[e] == sh.ctok[k];
-                const double w = again ? 0.0 : weight(warp == 0 ? sh.cz[k] : sh.cy[k], M, c, cf, sh.tab);
-                if (warp == 0) sh.ce[k] = w;
-                else sh.cq[k] = w;
-            }
-            __syncwarp();
-            if (warp == 0 && ids_only && lane == 0) {
-                // the mass before child k is what is not tried yet: base and the children from k on
-                double rest = S;
-                int acc = -1;
-                for (int k = nchild - 1; k >= 0; --k) {
-                    rest += sh.ce[k];
-                    if (static_cast<double>(sh.u[sh.child[k]]) * rest < sh.ce[k]) acc = k;
+        } else {
+            const bool use_q = prm.draft != nullptr && nchild > 0;
+            const bool ids_only = prm.draft == nullptr;
+            // The children's logits: lane k has child k's, in every warp (the few past 32 are read
+            // again where they are needed).  The largest is the reference to start from; a leaf
+            // takes the largest of the row's first 32.
+            const bool mine_q = use_q && lane < nchild;
+            const float cz = lane < nchild ? Logit<T>::load(zr, ctok[lane])
+                                           : nchild == 0 && lane < V ? Logit<T>::load(zr, lane) : -INFINITY;
+            const float cy = mine_q ? Logit<T>::load(yr, ctok[lane]) : -INFINITY;
+            float Mp = cz, Mq = cy, Mcta = 0.f;
+            for (int k = lane + 32; k < nchild; k += 32) Mp = fmaxf(Mp, Logit<T>::load(zr, ctok[k]));
+            Mp = warp_max(Mp);
+            if (use_q) Mq = warp_max(Mq);
+            // First in 32 bits, then, where that does not settle it, in 64.
+            double ip = 0.0, iq = 0.0, lam = 0.0, cta_p = 0.0, cta_r = 0.0;
+            bool residual = false;
+            for (bool exact = nchild == 0; acc < 0; exact = true) {
+                for (int which = 0; which < (use_q ? 2 : 1); ++which) {
+                    const char* row = which ? yr : zr;
+                    const int ndrop = ids_only ? nchild : 0;
+                    const float m = which ? Mq : Mp;
+                    const Part r = exact ? range_stats<T, kVec, true>(row, lo, hi, ctok, ndrop, m, c, sh.tab)
+                                         : range_stats<T, kVec, false>(row, lo, hi, ctok, ndrop, m, c, sh.tab);
+                    if (lane == 0) sh.warp[which][warp] = r;
                 }
-                sh.accepted = acc;
-            }
-        }
-        __syncthreads();
-        const float Mp = sh.M[0], Mq = sh.M[1];
-        const double ip = 1.0 / sh.S[0], iq = use_q ? 1.0 / sh.S[1] : 0.0;
-        parity ^= 1;
-        int acc = ids_only ? sh.accepted : -1;
-        double lam = 0.0;
-        bool residual = false;
-        if (use_q) {
-            double nrm = 1.0;
-            for (int k = 0; k < nchild; ++k) {
-                const double p = sh.ce[k] * ip, q = sh.cq[k] * iq;
-                if (static_cast<double>(sh.u[sh.child[k]]) * nrm * q < fmax(0.0, p - lam * q)) {
-                    acc = k;
-                    break;
-                }
-                lam += nrm;
-                const double w = range_residual<T, kVec>(zr, yr, lo, hi, Mp, Mq, ip, lam * iq, c, sh.tab);
-                if (lane == 0) sh.wres[warp] = w;
                 __syncthreads();
-                if (warp == 0 && lane < static_cast<int>(C)) {
-                    double t = 0.0;
-                    for (int i = 0; i < kTvWarps; ++i) t += sh.wres[i];
-                    st_cluster_u64(&sh.ex[parity][rank][0].s, lane, __double_as_longlong(t));
-                }
+                if (warp < (use_q ? 2 : 1)) exchange(warp, exact);
                 cluster_barrier();
-                nrm = 0.0;
-                for (uint32_t r = 0; r < C; ++r) nrm += sh.ex[parity][r][0].s;
-                residual = nrm > 0.0;
-                if (residual && tid < static_cast<int>(C)) sh.cta_r[tid] = sh.ex[parity][tid][0].s;
-                parity ^= 1;
-            }
-            __syncthreads();
-        }
-        if (acc >= 0) {
-            node = sh.child[acc];
-            if (rank == 0 && tid == 0) {
-                out_tok[j] = sh.tok[node];
-                out_path[j + 1] = node;
-            }
-            ++j;
-            __syncthreads();  // the lists are rebuilt
-            continue;
-        }
-
-        // The final draw: CTA, then warp, then element.
-        // (a residual without mass falls back to p)
-        const double* cta_w = residual ? sh.cta_r : sh.cta_p;
-        double W = 0.0;
-        for (uint32_t r = 0; r < C; ++r) W += cta_w[r];
-        const double want = static_cast<double>(sh.u[0]) * W;
-        double before = 0.0, rest = 0.0;
-        int owner = -1;
-        {
-            double cum = 0.0;
-            for (int r = 0; r < static_cast<int>(C); ++r) {
-                const double w = cta_w[r];
-                if (w > 0.0) {
-                    owner = r;
-                    before = cum;
-                }
-                cum += w;
-                if (cum > want) break;
-            }
-            rest = want - before;
-        }
-        if (owner < 0 && rank == 0 && tid == 0) out_tok[j] = nchild > 0 ? sh.ctok[0] : 0;
-        if (owner != static_cast<int>(rank)) break;
-        int from = 0;
-        {
-            double cum = 0.0, left = 0.0;
-            for (int w = 0; w < kTvWarps; ++w) {
-                double x;
-                if (residual) x = sh.wres[w];
-                else x = sh.warp[0][w].m == -INFINITY ? 0.0
-                                                      : sh.warp[0][w].s * weight(sh.warp[0][w].m, Mp, c, cf, sh.tab);
-                if (x > 0.0) {
-                    from = w;
-                    left = cum;
-                }
-                cum += x;
-                if (cum > rest) break;
-            }
-            rest -= left;
-        }
-        const int64_t rlo64 = (int64_t(rank) * kTvWarps + from) * prm.range;
-        const int rlo = static_cast<int>(rlo64 < V ? rlo64 : V);
-        const int rhi = rlo + prm.range < V ? rlo + prm.range : V;
-        const int each = (rhi - rlo + kTvThreads - 1) / kTvThreads;
-        auto draw_weight = [&](int v) {
-            double w = weight(Logit<T>::load(zr, v), Mp, c, cf, sh.tab);
-            if (residual) return fmax(0.0, w * ip - weight(Logit<T>::load(yr, v), Mq, c, cf, sh.tab) * (lam * iq));
-            if (ids_only)
-                for (int k = 0; k < nchild; ++k)
-                    if (sh.ctok[k] == v) w = 0.0;
-            return w;
-        };
-        const int v0 = rlo + tid * each, v1 = v0 + each < rhi ? v0 + each : rhi;
-        double mine = 0.0;
-        for (int v = v0; v < v1; ++v) mine += draw_weight(v);
-        double incl = mine;
+                const double Sp = row_sum(0, exact, &Mp, &cta_p);
+                Mcta = sh.ex[parity][rank][0].m;
+                if (ids_only) {
+                    // The mass before child k is what is not tried yet: base and the children from k
+                    // on.  Children in lanes, chunks from the last to the first; -2: too near to tell.
+                    const double above = exact ? 1.0 : 1.0 + kFastError, below = exact ? 1.0 : 1.0 - kFastError;
+                    double rest = Sp;
+                    for (int k0 = (nchild - 1) & ~31; k0 >= 0 && nchild > 0; k0 -= 32) {
+                        const int k = k0 + lane, n = nchild - k0 < 32 ? nchild - k0 : 32;
+                        const bool has = k < nchild;
+                        const int t = has ? ctok[k] : -1;
+                        bool again = false;  // a sibling's token again: nothing of it is left
+                        for (int e = 0; e + 1 < n; ++e) {
+                            const int other = __shfl_sync(0xffffffffu, t, e);
+                            again |= lane > e && other == t;
+                        }
+                        for (int e = 0; e < k0; ++e) again |= ctok[e] == t;
+                        double w = 0.0;
+                        bool faint = false;  // too small for 32 bits
+                        if (has && !again) {
+                            const float z = k0 == 0 ? cz : Logit<T>::load(zr, t);
+                            w = exact ? weight(z, Mp, c, cf, sh.tab) : static_cast<double>(ex2_approx((z - Mp) * cf));
+                            faint = !exact && (z - Mp) * cf < kFaint;
+                        }
+                        double from = w;  // of the children from k on, in this chunk
+                        for (int o = 1; o < n; o <<= 1) {
+                            const double x = __shfl_down_sync(0xffffffffu, from, o);
+                            if (lane + o < 32) from += x;
+                        }
+                        const double x = has ? static_cast<double>(sh.u[child[k]]) * (rest + from) : 0.0;
+                        const uint32_t yes = __ballot_sync(0xffffffffu, has && x * above < w);
+                        const uint32_t may = __ballot_sync(0xffffffffu, has && (x * below < w || faint));
+                        if (may) acc = yes && __ffs(yes) == __ffs(may) ? k0 + __ffs(yes) - 1 : -2;
+                        rest += __shfl_sync(0xffffffffu, from, 0);
+                    }
+                } else if (use_q) {
+                    double cta_q;
+                    const double Sq = row_sum(1, exact, &Mq, &cta_q);
+                    if (!exact) {
+                        // the first child's test: u q < p
+                        const double x = static_cast<double>(sh.u[child[0]]) * ex2_approx((cy - Mq) * cf) * Sp;
+                        const bool yes = x * (1.0 + 4.0 * kFastError) < ex2_approx((cz - Mp) * cf) * Sq &&
+                                         (cy - Mq) * cf >= kFaint && (cz - Mp) * cf >= kFaint;
+                        if (__shfl_sync(0xffffffffu, int(yes), 0)) acc = 0;
+                    } else {
+                        ip = 1.0 / Sp;
+                        iq = 1.0 / Sq;
+                        for (int k = tid; k < nchild; k += kTvThreads) {
+                            sh.ce[k] = weight(Logit<T>::load(zr, ctok[k]), Mp, c, cf, sh.tab) * ip;
+                            sh.cq[k] = weight(Logit<T>::load(yr, ctok[k]), Mq, c, cf, sh.tab) * iq;
+                        }
+                        __syncthreads();
+                        double nrm = 1.0;
+                        for (int k = 0; k < nchild; ++k) {
+                            const double p = sh.ce[k], q = sh.cq[k];
+                            if (static_cast<double>(sh.u[child[k]]) * nrm * q < fmax(0.0, p - lam * q)) {
+                                acc = k;
+                                break;
+                            }
+                            lam += nrm;
+                            parity ^= 1;
+                            const double w = range_residual<T, kVec>(zr, yr, lo, hi, Mp, Mq, ip, lam * iq, c, sh.tab);
+                            if (lane == 0) sh.wres[warp] = w;
+                            __syncthreads();
+                            if (warp == 0) {
+                                double t = sh.wres[lane % kTvWarps];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) sh.wscan[warp] = incl;
-        if (tid == 0) sh.pick = 0x7fffffff;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += sh.wscan[w];
-        // the first thread whose running sum passes; else the last with weight
-        if (mine > 0.0 && incl > rest) atomicMin(&sh.pick, tid);
-        __syncthreads();
-        if (sh.pick == 0x7fffffff) {
-            __syncthreads();
-            if (tid == 0) sh.pick = -1;
-            __syncthreads();
-            if (mine > 0.0) atomicMax(&sh.pick, tid);
-            __syncthreads();
-        }
-        if (tid == sh.pick) {
-            double run = incl - mine;
-            int t = v0;
-            for (int v = v0; v < v1; ++v) {
-                const double w = draw_weight(v);
-                run += w;
-                if (w > 0.0) {
-                    t = v;
-                    if (run > rest) break;
+                                for (int o = kTvWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                                if (lane < C) st_cluster_u64(&sh.ex[parity][rank][0].s, lane, __double_as_longlong(t));
+                            }
+                            cluster_barrier();
+                            cta_r = nrm = sh.ex[parity][lane & (C - 1)][0].s;
+                            for (int o = C >> 1; o > 0; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
+                            residual = nrm > 0.0;
+                        }
+                    }
                 }
+                parity ^= 1;
+                if (exact) break;
             }
-            out_tok[j] = t;
+            if (acc < 0) {
+                // The final draw: CTA, then warp, then element (a residual without mass falls back to p).
+                const double cta = lane < C ? (residual ? cta_r : cta_p) : 0.0;
+                double W = cta;
+                for (int o = kTvMaxCluster / 2; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+                double rest = static_cast<double>(sh.u[0]) * __shfl_sync(0xffffffffu, W, 0);
+                const int owner = pick_entry(cta, C, &rest);
+                if (owner < 0 && rank == 0 && tid == 0) out_tok[j] = nchild > 0 ? ctok[0] : 0;
+                if (owner != rank) break;
+                const double f = residual ? 1.0 : rescale<true>(1.0, Mcta, Mp, c, cf, sh.tab);
+                const int from = pick_entry(lane < kTvWarps ? (residual ? sh.wres[lane] : sh.wp[lane]) * f : 0.0,
+                                            kTvWarps, &rest);
+                const int64_t rlo64 = (int64_t(rank) * kTvWarps + from) * prm.range;
+                const int rlo = static_cast<int>(rlo64 < V ? rlo64 : V);
+                const int rhi = rlo + prm.range < V ? rlo + prm.range : V;
+                // thread i sums elements [i each, (i + 1) each) of the range
+                const int each = (rhi - rlo + kTvThreads - 1) / kTvThreads;
+                const int v0 = rlo + tid * each, v1 = v0 + each < rhi ? v0 + each : rhi;
+                auto draw_weight = [&](int v) {
+                    double w = weight(Logit<T>::load(zr, v), Mp, c, cf, sh.tab);
+                    if (residual) w = fmax(0.0, w * ip - weight(Logit<T>::load(yr, v), Mq, c, cf, sh.tab) * (lam * iq));
+                    if (ids_only)
+                        for (int k = 0; k < nchild; ++k)
+                            if (ctok[k] == v) w = 0.0;
+                    return w;
+                };
+                double mine = 0.0;
+#pragma unroll 1
+                for (int v = v0; v < v1; ++v) mine += draw_weight(v);
+                const double sum = warp_sum(mine);
+                if (lane == 0) sh.wscan[warp] = sum;
+                __syncthreads();
+                const int at = pick_entry(lane < kTvWarps ? sh.wscan[lane] : 0.0, kTvWarps, &rest);
+                if (at < 0 && tid == 0) out_tok[j] = rlo < V ? rlo : V - 1;
+                if (warp == at) {
+                    // that thread's elements, a lane each
+                    const int src = pick_entry(mine, 32, &rest);
+                    int t = rlo;
+                    const int p0 = __shfl_sync(0xffffffffu, v0, src), p1 = __shfl_sync(0xffffffffu, v1, src);
+#pragma unroll 1
+                    for (int v = p0; v < p1; v += 32) {
+                        const double w = v + lane < p1 ? draw_weight(v + lane) : 0.0;
+                        const double all = warp_sum(w);
+                        double left = rest;
+                        bool passed;
+                        const int i = pick_entry(w, 32, &left, &passed);
+                        if (i >= 0) t = v + i;
+                        if (passed) break;
+                        rest -= all;
+                    }
+                    if (lane == 0) out_tok[j] = t;
+                }
+                break;
+            }
         }
-        break;
+        node = child[acc];
+        if (rank == 0 && tid == 0) {
+            out_tok[j] = sh.tok[node];
+            out_path[j + 1] = node;
+        }
+        ++j;
     }
     if (rank == 0) {
         for (int i = tid; i < N; i += kTvThreads) {
@@ -554,26 +679,27 @@ __global__ void __launch_bounds__(kTvThreads) tree_verify_kernel(const TreeVerif
     }
 }
 
-// CTAs per request: as many as let all requests run at once (two CTAs per
-// SM), no more than the row has 4 KiB pieces for.
+// CTAs per request: as many as let all requests run at once, no more than
+// the row has 4 KiB pieces for.
 int cluster_for(int B, int V, int es, int sms) {
     int c = kTvMaxCluster;
-    while (c > 1 && (int64_t(B) * c > 2 * int64_t(sms) || int64_t(c / 2) * 4096 >= int64_t(V) * es)) c /= 2;
+    while (c > 1 && (int64_t(B) * c > kTvCtasPerSm * int64_t(sms) || int64_t(c / 2) * 4096 >= int64_t(V) * es)) c /= 2;
     return c;
 }
 
 template <typename T, bool kVec, bool kGreedy>
 cudaError_t launch(TreeVerifyParams prm, int B, cudaStream_t st) {
-    auto k = tree_verify_kernel<T, kVec, kGreedy>;
     TreeDevice dev;
     cudaError_t e = tree_device(&dev);
     if (e != cudaSuccess) return e;
     const int C = cluster_for(B, prm.V, Logit<T>::kSize, dev.sm_count);
+    const bool roomy = int64_t(B) * C <= 2 * int64_t(dev.sm_count);
+    auto k = roomy ? tree_verify_kernel<T, kVec, kGreedy, 2> : tree_verify_kernel<T, kVec, kGreedy, kTvCtasPerSm>;
     if (C > 8) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-    const int step = Batch<T, kVec>::kStep / kTvUnroll;  // a warp's vector step
+    const int step = Batch<T, kVec, 1>::kStep;  // a warp's vector
     const int64_t warps = int64_t(C) * kTvWarps;
     prm.range = static_cast<int>(((prm.V + warps - 1) / warps + step - 1) / step * step);
     return launch_dependent(k, dim3(static_cast<unsigned>(int64_t(B) * C)), kTvThreads, 0, C, st, prm);
@@ -594,7 +720,7 @@ extern "C" sv_status sv_tree_verify(const sv_tree_shape* s, const void* target, 
     if (stride < s->V) return SV_EINVAL;
     if (!target || !tokens || !out_accept_len || !out_tokens || !out_path) return SV_EINVAL;
     if (!greedy && (!uniforms || !(temperature > 0.0) || !std::isfinite(temperature) ||
-                    !std::isfinite(1.4426950408889634 / temperature)))
+                    !std::isnormal(static_cast<float>(1.4426950408889634 / temperature))))
         return SV_EINVAL;
     if (s->B == 0) return SV_OK;
     if (int64_t(s->B) * kTvMaxCluster > 0x7fffffff) return SV_EUNSUPPORTED;
