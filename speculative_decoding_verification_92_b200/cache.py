@@ -16,8 +16,11 @@ synchronises, so a whole step can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from . import BF16, F32, _check, _torch, library
+import torch
+
+from . import BF16, F32, SpecVerifyError, library
 
 __all__ = ["cache_resize", "cache_commit", "cache_fork", "F16", "MAX_SLOTS"]
 
@@ -27,17 +30,15 @@ MAX_SLOTS = 8192    # SV_MAX_SLOTS of the C header
 _VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", _VP), ("v", _VP), ("layers", _I32), ("pages", _I32), ("page_size", _I32), ("heads", _I32),
-                ("head_dim", _I32), ("dtype", _I32), ("layer_stride", _I64), ("page_stride", _I64),
-                ("row_stride", _I64), ("head_stride", _I64)]
-
-
+# sv_cache, packed: k, v, five int32 (layers, pages, page_size, heads,
+# head_dim), dtype, four int64 strides.
+_CACHE = struct.Struct("@2P6i4q")
 _SIGNATURES = {
-    "sv_cache_commit": (_I32, [ctypes.POINTER(_Cache), _VP, _I64, _I32, _I32, _VP, _VP, _I64, _I32, _VP, _VP]),
+    "sv_cache_commit": (_I32, [ctypes.c_char_p, _VP, _I64, _I32, _I32, _VP, _VP, _I64, _I32, _VP, _VP]),
     "sv_cache_resize": (_I32, [_VP, _I64, _I32, _I32, _VP, _I32, _VP, _I32, _VP, _VP]),
-    "sv_cache_fork": (_I32, [ctypes.POINTER(_Cache), _VP, _I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP]),
+    "sv_cache_fork": (_I32, [ctypes.c_char_p, _VP, _I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP]),
 }
+_KV_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _LIB = None
 
 
@@ -52,68 +53,71 @@ def _library():
     return _LIB
 
 
-def _kv_code(t) -> int:
-    torch = _torch()
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"the cache must be float32, bfloat16 or float16, got {t.dtype}")
-    return code
+def _bad_tensor(what, t, dtype, shape, device, layout):
+    """Raises what is wrong with a tensor that did not pass a quick check."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected the device of the call ({device})")
+    raise ValueError(f"{what} must {layout}")
 
 
-def _ints(what, t, shape, device, rows=False):
-    """Pointer of an int32 tensor of exactly this shape (contiguous, or with
-    ``rows`` any stride between contiguous rows); None passes through."""
+def _dense(what, t, dtype, shape, device):
+    """Pointer of a contiguous tensor of exactly this dtype, shape and device;
+    None passes through.  Calls of a few microseconds are checked here, so the
+    usual case is one expression."""
     if t is None:
         return None
-    if t.dtype != _torch().int32:
-        raise TypeError(f"{what} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{what} is on {t.device}, expected the CUDA device of the call ({device})")
-    if rows:
-        if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1):
-            raise ValueError(f"{what} must have contiguous rows that do not overlap")
-    elif not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _bad_tensor(what, t, dtype, shape, device, "be contiguous")
 
 
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _int_rows(what, t, shape, device):
+    """Pointer and row stride of an int32 matrix with contiguous rows."""
+    if t.dtype == torch.int32 and t.shape == shape and t.device == device:
+        s0, s1 = t.stride()
+        if s1 == 1 or shape[1] <= 1:
+            if shape[0] <= 1:
+                return t.data_ptr(), shape[1]
+            if s0 >= shape[1]:
+                return t.data_ptr(), s0
+    _bad_tensor(what, t, torch.int32, shape, device, "have contiguous rows that do not overlap")
 
 
-def _cache(k, v) -> _Cache:
+def _cache(k, v) -> bytes:
     """The C description of a cache; 4-d tensors are one layer."""
-    if k.dim() not in (4, 5) or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+    shape, st, dtype = k.shape, k.stride(), k.dtype
+    if (len(shape) not in (4, 5) or v.shape != shape or v.dtype != dtype or v.device != k.device
+            or v.stride() != st or (st[-1] != 1 and shape[-1] > 1)):
         raise ValueError("k_cache and v_cache must be [layers, pages, page_size, heads, head_dim] tensors of one "
-                         "shape, dtype and device")
-    if k.stride() != v.stride() or (k.stride(-1) != 1 and k.shape[-1] > 1):
-        raise ValueError("k_cache and v_cache must have the same strides and a contiguous last dimension")
-    if not k.is_cuda:
-        raise ValueError("k_cache and v_cache must be CUDA tensors")
-    shape = k.shape if k.dim() == 5 else (1, *k.shape)
-    st = k.stride() if k.dim() == 5 else (0, *k.stride())
-    return _Cache(k.data_ptr(), v.data_ptr(), *shape, _kv_code(k), *(s if n > 1 else 0 for s, n in zip(st[:4], shape)))
+                         "shape, dtype, device and layout with a contiguous last dimension")
+    if dtype not in _KV_CODES:
+        raise TypeError(f"the cache must be float32, bfloat16 or float16, got {dtype}")
+    if len(shape) == 4:
+        shape, st = (1, *shape), (0, *st)
+    s0, s1, s2, s3, _ = st
+    n0, n1, n2, n3, n4 = shape
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), n0, n1, n2, n3, n4, _KV_CODES[dtype], s0 if n0 > 1 else 0,
+                       s1 if n1 > 1 else 0, s2 if n2 > 1 else 0, s3 if n3 > 1 else 0)
 
 
-class _on:
-    """Makes the tensors' device current for a call and gives its stream."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = _torch().cuda.current_stream(self.device) if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _call(fn, device, stream, *args):
+    """The C call with the tensors' device current, on `stream` or the device's
+    current stream."""
+    index = device.index
+    if index is None:
+        raise ValueError(f"{fn.__name__} needs CUDA tensors, got tensors on {device}")
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status:
+        raise SpecVerifyError(status, fn.__name__)
 
 
 def _table(page_table):
@@ -131,17 +135,16 @@ def cache_resize(page_table, lens, refcount, page_size, *, status=None, stream=N
     valid, or the free pages did not reach it)."""
     slots, max_pages = _table(page_table)
     dev = page_table.device
-    lib = _library()
     if status is None:
-        status = _torch().empty(slots, dtype=_torch().int32, device=dev)
-    if refcount.dim() != 1:
+        status = torch.empty(slots, dtype=torch.int32, device=dev)
+    pages = refcount.shape
+    if len(pages) != 1:
         raise ValueError("refcount must be [pages]")
-    args = (_ints("page_table", page_table, (slots, max_pages), dev, rows=True), _row_stride(page_table), slots,
-            max_pages, _ints("lens", lens, (slots,), dev), int(page_size),
-            _ints("refcount", refcount, refcount.shape, dev), refcount.shape[0],
-            _ints("status", status, (slots,), dev))
-    with _on(dev, stream) as st:
-        _check(lib.sv_cache_resize(*args, st), "sv_cache_resize")
+    table, stride = _int_rows("page_table", page_table, (slots, max_pages), dev)
+    _call(_library().sv_cache_resize, dev, stream, table, stride, slots, max_pages,
+          _dense("lens", lens, torch.int32, (slots,), dev), int(page_size),
+          _dense("refcount", refcount, torch.int32, pages, dev), pages[0],
+          _dense("status", status, torch.int32, (slots,), dev))
     return status
 
 
@@ -153,19 +156,19 @@ def cache_commit(k_cache, v_cache, page_table, lens, path, *, out_lens=None, str
     was left alone); ``out_lens`` must be another tensor than ``lens``."""
     B, max_pages = _table(page_table)
     dev = page_table.device
-    lib = _library()
     c = _cache(k_cache, v_cache)
     if out_lens is None:
-        out_lens = _torch().empty(B, dtype=_torch().int32, device=dev)
+        out_lens = torch.empty(B, dtype=torch.int32, device=dev)
     if path.dim() != 2:
         raise ValueError("path must be [B, width]")
     if k_cache.device != dev:
         raise ValueError(f"the cache is on {k_cache.device}, page_table on {dev}")
-    args = (ctypes.byref(c), _ints("page_table", page_table, (B, max_pages), dev, rows=True), _row_stride(page_table),
-            B, max_pages, _ints("lens", lens, (B,), dev), _ints("path", path, (B, path.shape[1]), dev, rows=True),
-            _row_stride(path), path.shape[1], _ints("out_lens", out_lens, (B,), dev))
-    with _on(dev, stream) as st:
-        _check(lib.sv_cache_commit(*args, st), "sv_cache_commit")
+    width = path.shape[1]
+    table, stride = _int_rows("page_table", page_table, (B, max_pages), dev)
+    rows, path_stride = _int_rows("path", path, (B, width), dev)
+    _call(_library().sv_cache_commit, dev, stream, c, table, stride, B, max_pages,
+          _dense("lens", lens, torch.int32, (B,), dev), rows, path_stride, width,
+          _dense("out_lens", out_lens, torch.int32, (B,), dev))
     return out_lens
 
 
@@ -177,7 +180,6 @@ def cache_fork(k_cache, v_cache, page_table, lens, refcount, src, dst, *, status
     nothing changed) or -2 (no free page left: ``dst`` is left empty)."""
     slots, max_pages = _table(page_table)
     dev = page_table.device
-    lib = _library()
     c = _cache(k_cache, v_cache)
     if src.dim() != 1:
         raise ValueError("src must be [forks]")
@@ -185,11 +187,11 @@ def cache_fork(k_cache, v_cache, page_table, lens, refcount, src, dst, *, status
         raise ValueError(f"the cache is on {k_cache.device}, page_table on {dev}")
     n = src.shape[0]
     if status is None:
-        status = _torch().empty(n, dtype=_torch().int32, device=dev)
-    args = (ctypes.byref(c), _ints("page_table", page_table, (slots, max_pages), dev, rows=True),
-            _row_stride(page_table), slots, max_pages, _ints("lens", lens, (slots,), dev),
-            _ints("refcount", refcount, (c.pages,), dev), _ints("src", src, (n,), dev), _ints("dst", dst, (n,), dev), n,
-            _ints("status", status, (n,), dev))
-    with _on(dev, stream) as st:
-        _check(lib.sv_cache_fork(*args, st), "sv_cache_fork")
+        status = torch.empty(n, dtype=torch.int32, device=dev)
+    table, stride = _int_rows("page_table", page_table, (slots, max_pages), dev)
+    pages = k_cache.shape[-4]
+    _call(_library().sv_cache_fork, dev, stream, c, table, stride, slots, max_pages,
+          _dense("lens", lens, torch.int32, (slots,), dev), _dense("refcount", refcount, torch.int32, (pages,), dev),
+          _dense("src", src, torch.int32, (n,), dev), _dense("dst", dst, torch.int32, (n,), dev), n,
+          _dense("status", status, torch.int32, (n,), dev))
     return status

@@ -68,7 +68,7 @@ struct AttnParams {
     const int32_t* counts;
     float scale;
     int32_t slot_rows;  // rows of a partial result
-    int32_t* rows;      // [B] cached rows lens + count of a request to compute, 0 = none
+    int32_t* ok;        // [B] the request passed all checks
     uint32_t* masks;    // [B][N][kMaskWords] ancestors-or-self of each node
     int32_t* odd;       // [B][N] the node's value row is not finite
     float2* part_ml;    // [2 CTAs][slot_rows] reference and sum,
@@ -86,7 +86,7 @@ struct Half<__nv_bfloat16> {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    __device__ static float sum(uint32_t w) { return bf16_lo(w) + bf16_hi(w); }
+    __device__ static uint64_t widen(uint32_t w) { return bf16x2_to_f2(w); }
 };
 template <>
 struct Half<__half> {
@@ -99,9 +99,9 @@ struct Half<__half> {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    __device__ static float sum(uint32_t w) {
+    __device__ static uint64_t widen(uint32_t w) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        return f.x + f.y;
+        return f2_pack(f.x, f.y);
     }
 };
 
@@ -111,11 +111,21 @@ struct Half<__half> {
 __device__ __forceinline__ int groups_of(const AttnParams& a, int count) {
     return (count * (a.q_heads / a.heads) + kUnitRows - 1) / kUnitRows;
 }
+// Cached rows of request b with its nodes, 0 where there is nothing to do
+// (what tree_prepare_kernel finds wrong beyond this is left to it).
+__device__ __forceinline__ int rows_of(const AttnParams& a, int b, int* len) {
+    const int count = a.counts ? a.counts[b] : a.N;
+    *len = a.lens[b];
+    const int64_t rows = int64_t(*len) + count;
+    const bool fits = count > 0 && count <= a.N && *len >= 0 && rows <= int64_t(a.max_pages) * a.page_size;
+    return fits ? static_cast<int>(rows) : 0;
+}
 // Tiles of request b's units.
 __device__ __forceinline__ int64_t tiles_of(const AttnParams& a, int b) {
-    const int rows = a.rows[b];
+    int len;
+    const int rows = rows_of(a, b, &len);
     if (rows == 0) return 0;
-    return int64_t((rows + kTile - 1) / kTile) * a.heads * groups_of(a, rows - a.lens[b]);
+    return int64_t((rows + kTile - 1) / kTile) * a.heads * groups_of(a, rows - len);
 }
 // Sums of v over the threads before this one and over all (whole warps).
 template <int kThreads>
@@ -150,12 +160,12 @@ struct PieceIter {
     int64_t left;  // tiles left in the run
     __device__ bool next(const AttnParams& a, Piece& p) {
         if (left <= 0) return false;
-        int rows;
-        while ((rows = a.rows[b]) == 0) {
+        int rows, len;
+        while ((rows = rows_of(a, b, &len)) == 0) {
             ++b;
             rem = 0;
         }
-        const int len = a.lens[b], g = a.q_heads / a.heads, R = (rows - len) * g;
+        const int g = a.q_heads / a.heads, R = (rows - len) * g;
         const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
         const int unit = rem / tiles;
         p.b = b;
@@ -236,9 +246,9 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             mbar_init(&ctl.vempty[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&ctl.qfull[t], kTile);
+            mbar_init(&ctl.qfull[t], kTile / 32);
             mbar_init(&ctl.sfull[t], 1);
-            mbar_init(&ctl.pfull[t], kTile);
+            mbar_init(&ctl.pfull[t], kTile / 32);
             mbar_init(&ctl.ofull[t], 1);
         }
         fence_mbar_init();
@@ -247,8 +257,11 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     }
     if (warp == 9) tmem_alloc(&ctl.tmem, 512);
     if (tid == 0) ctl.left = 0;
-    grid_dependency_wait();
     grid_launch_dependents();
+    // The kernel before this one (tree_prepare_kernel) lets this one start once all work before it
+    // is done: the inputs and the cached prefix can be read.  What it writes itself, the new rows
+    // and the checks, is waited for where it is read.
+    auto reads_new_rows = [](const Piece& p, int tile) { return (tile + 1) * kTile > p.len; };
 
     // this CTA's run of tiles
     {
@@ -280,49 +293,55 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     Piece p{};
 
     if (warp == 8) {
-        // ---- loads
-        if (lane == 0) {
-            uint32_t kn = 0, vn = 0;  // tiles issued
-            bool ok = true;
-            const int per_tile = kTile / a.page_size;
-            auto load = [&](const CUtensorMap* map, unsigned char* dst, uint64_t* bar, int tile) {
-                const int page0 = tile * per_tile;
-                const int used = (p.rows + a.page_size - 1) / a.page_size - page0;
-                const int n = used < per_tile ? used : per_tile;
-                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * a.page_size * D * 2));
-                const int32_t* ids = a.table + p.b * a.table_stride + page0;
-                for (int i = 0; i < n; ++i) {
-                    const int id = ids[i];
-                    for (int x = 0; x < D; x += 64)
-                        tma_load_4d(dst + (x / 64) * (kTile * 128) + i * a.page_size * 128, map, x, p.head, 0, id, bar);
+        // ---- loads: lane i has box i of a tile, 64 columns of a page
+        constexpr int kHalves = D / 64;
+        uint32_t kn = 0, vn = 0;  // tiles issued
+        bool ok = true;
+        const int per_tile = kTile / a.page_size;
+        const int page = lane / kHalves, x = lane % kHalves;
+        const uint32_t to = x * (kTile * 128) + page * a.page_size * 128;
+        auto wait_new_rows = [] {
+            grid_dependency_wait();
+            asm volatile("fence.proxy.async;" ::: "memory");
+        };
+        // the page id of this lane's box in a tile (-1: none)
+        auto page_id = [&](int tile) {
+            const int at = tile * per_tile + page;
+            return page < per_tile && at * a.page_size < p.rows ? a.table[p.b * a.table_stride + at] : -1;
+        };
+        auto load = [&](const CUtensorMap* map, unsigned char* ring, uint64_t* full, uint64_t* empty, uint32_t stages,
+                        uint32_t& n, int id) {
+            const uint32_t s = n % stages;
+            ok = ok && (n < stages || mbar_wait_bounded(empty + s, (n / stages - 1) & 1, kAttendTimeoutNs));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            const int boxes = __popc(__ballot_sync(0xffffffffu, id >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(boxes * a.page_size * 128));
+            __syncwarp();
+            if (id >= 0) tma_load_4d(ring + s * TB + to, map, x * 64, p.head, 0, id, full + s);
+            ++n;
+        };
+        while (ok && it.next(a, p)) {
+            int id = page_id(p.first), next = p.n > 1 ? page_id(p.first + 1) : -1;
+            if (reads_new_rows(p, p.first)) wait_new_rows();
+            load(&kmap, ks, ctl.kfull, ctl.kempty, KS, kn, id);
+            for (int i = 0; i < p.n && ok; ++i) {
+                const int after = i + 2 < p.n ? page_id(p.first + i + 2) : -1;
+                if (i + 1 < p.n) {
+                    if (reads_new_rows(p, p.first + i + 1)) wait_new_rows();
+                    load(&kmap, ks, ctl.kfull, ctl.kempty, KS, kn, next);
                 }
-            };
-            auto load_k = [&](int tile) {
-                const uint32_t s = kn % KS;
-                ok = ok && (kn < KS || mbar_wait_bounded(&ctl.kempty[s], (kn / KS - 1) & 1, kAttendTimeoutNs));
-                if (ok) load(&kmap, ks + s * TB, &ctl.kfull[s], tile);
-                kn += ok;
-            };
-            auto load_v = [&](int tile) {
-                const uint32_t s = vn % VS;
-                ok = ok && (vn < VS || mbar_wait_bounded(&ctl.vempty[s], (vn / VS - 1) & 1, kAttendTimeoutNs));
-                if (ok) load(&vmap, vs + s * TB, &ctl.vfull[s], tile);
-                vn += ok;
-            };
-            while (ok && it.next(a, p)) {
-                load_k(p.first);
-                for (int i = 0; i < p.n; ++i) {
-                    if (i + 1 < p.n) load_k(p.first + i + 1);
-                    load_v(p.first + i);
-                }
+                load(&vmap, vs, ctl.vfull, ctl.vempty, VS, vn, id);
+                id = next;
+                next = after;
             }
-            // a wait ran out: nothing may be in flight when the CTA ends
-            if (!ok) {
-                for (uint32_t i = kn > KS ? kn - KS : 0; i < kn; ++i)
-                    mbar_wait_bounded(&ctl.kfull[i % KS], (i / KS) & 1, kAttendTimeoutNs);
-                for (uint32_t i = vn > VS ? vn - VS : 0; i < vn; ++i)
-                    mbar_wait_bounded(&ctl.vfull[i % VS], (i / VS) & 1, kAttendTimeoutNs);
-            }
+        }
+        // a wait ran out: nothing may be in flight when the CTA ends
+        if (!ok) {
+            for (uint32_t i = kn > KS ? kn - KS : 0; i < kn; ++i)
+                mbar_wait_bounded(&ctl.kfull[i % KS], (i / KS) & 1, kAttendTimeoutNs);
+            for (uint32_t i = vn > VS ? vn - VS : 0; i < vn; ++i)
+                mbar_wait_bounded(&ctl.vfull[i % VS], (i / VS) & 1, kAttendTimeoutNs);
         }
     } else if (warp == 9) {
         // ---- matrix products
@@ -434,7 +453,8 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     *reinterpret_cast<uint4*>(dst + (x / 8) * (kTile * 128) + (((x % 8) ^ (r & 7)) * 16)) = w;
                 }
                 fence_async_shared();
-                mbar_arrive(&ctl.qfull[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.qfull[t]);
             }
             const uint32_t* mask = a.masks + (int64_t(p.b) * a.N + (valid ? node : 0)) * kMaskWords;
             float m = -INFINITY, l = 0.f;
@@ -442,7 +462,8 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             bool odd = false;
             for (int i = from; i < p.n; i += step) {
                 const int pos0 = (p.first + i) * kTile;
-                const bool tail = pos0 + kTile > p.len;          // holds rows of the tree, or past it
+                const bool tail = reads_new_rows(p, p.first + i);  // holds rows of the tree, or past it
+                if (tail) grid_dependency_wait();
                 // (after a wait that ran out every barrier is still met, so that no thread waits for good)
                 const int parity = sn & 1;
                 ok = ok && mbar_wait_bounded(&ctl.sfull[t], parity, kAttendTimeoutNs);
@@ -473,22 +494,32 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                 ok = __all_sync(0xffffffffu, ok);
                 tcgen05_fence_after();
                 if (live && ok) {
-                    uint32_t s[128];
-                    tmem_load(s, lanes + s_at(t));
+                    // which columns this row sees, 32 to a word
+                    uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                     if (tail) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const uint32_t see = mask_word(mask, pos0 + 32 * w - p.len);
-                            odd |= (see & ctl.odd[t][parity][w]) != 0;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(see >> k & 1u)) s[32 * w + k] = 0xff800000u;
+                            see[w] = mask_word(mask, pos0 + 32 * w - p.len);
+                            odd |= (see[w] & ctl.odd[t][parity][w]) != 0;
                         }
                     }
+                    // the scores are read twice, for the maximum and for the weights: tensor
+                    // memory is faster than 128 registers are cheap
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(s[k]));
-                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c - H::kShift;
+                    for (int w = 0; w < 4; w += 2) {
+                        uint32_t s[64];
+                        tmem_load(s, lanes + s_at(t) + 32 * w);
+                        if (tail) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (!(see[w + k / 32] >> (k % 32) & 1u)) s[k] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 64; k += 2)
+                            m4[k / 2 & 3] = max3(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), m4[k / 2 & 3]);
+                    }
+                    const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * c - H::kShift;
                     const bool rise = i == from ? top > m : top > m + 8.f;
                     if (__any_sync(0xffffffffu, rise)) {
                         const float f = top > m ? ex2_approx(m - top) : 1.f;   // 0 where there was nothing yet
@@ -506,24 +537,35 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;  // a row that sees nothing here: all weights 0
-                    float sum[2] = {0.f, 0.f};
+                    const uint64_t cc = f2_pack(c, c), mm = f2_pack(-ref, -ref);
+                    uint64_t sum = f2_pack(0.f, 0.f);
+                    // (the weights of columns 32 w .. go over scores that have been read)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t w[32];
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t s[32], packed[16];
+                        tmem_load(s, lanes + s_at(t) + 32 * w);
+                        if (tail) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float x = ex2_approx(fmaf(__uint_as_float(s[64 * half + 2 * k]), c, -ref));
-                            const float y = ex2_approx(fmaf(__uint_as_float(s[64 * half + 2 * k + 1]), c, -ref));
-                            w[k] = H::pack(x, y);
-                            sum[k & 1] += H::sum(w[k]);
+                            for (int k = 0; k < 32; ++k)
+                                if (!(see[w] >> k & 1u)) s[k] = 0xff800000u;
                         }
-                        tmem_store(lanes + s_at(t) + 32 * half, w);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float x, y;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, mm), x, y);
+                            packed[k / 2] = H::pack(ex2_approx(x), ex2_approx(y));
+                            sum = f2_add(sum, H::widen(packed[k / 2]));
+                        }
+                        tmem_store(lanes + s_at(t) + 16 * w, packed);
                     }
-                    l += sum[0] + sum[1];
+                    float sx, sy;
+                    f2_unpack(sum, sx, sy);
+                    l += sx + sy;
                     tmem_wait_st();
                 }
                 tcgen05_fence_before();
-                mbar_arrive(&ctl.pfull[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.pfull[t]);
             }
             vn += p.n;
             if (odd || !ok) l = NAN;
@@ -550,7 +592,9 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     m = M;
                 }
             }
+            grid_dependency_wait();
             if (live && (t == 0 || !p.split)) {
+                const bool good = valid && a.ok[p.b] != 0;
                 const bool whole = p.n == p.tiles;
                 const int64_t slot = 2 * int64_t(blockIdx.x) + (p.first == 0);
                 const int slot_row = tile0 + r;
@@ -571,7 +615,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                             o[k] = __float_as_uint(y);
                         }
                     }
-                    if (valid && whole) {
+                    if (good && whole) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) {
                             uint4 w;
@@ -581,7 +625,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                                 wp[e] = H::pack(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
                             *reinterpret_cast<uint4*>(dst + (x + k) * 2) = w;
                         }
-                    } else if (valid) {
+                    } else if (good) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             a.part_o[(slot * (D / 4) + (x + k) / 4) * a.slot_rows + slot_row] =
@@ -596,6 +640,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             if (p.split) named_barrier_sync(3, 2 * kTile);       // O of group 1 and the exchange are read
         }
     }
+    grid_dependency_wait();  // this grid ends after the one before it
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
@@ -614,14 +659,19 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
     __shared__ int64_t sums[2][kJoinThreads / 32];
     const int b = blockIdx.x / units, unit = blockIdx.x % units;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dependency_wait();
-    const int rows = a.rows[b];
-    if (rows == 0) return;
-    const int len = a.lens[b], g = a.q_heads / a.heads, R = (rows - len) * g;
+    int len;
+    const int rows = rows_of(a, b, &len);
+    if (rows == 0) {
+        grid_dependency_wait();
+        return;
+    }
+    const int g = a.q_heads / a.heads, R = (rows - len) * g;
     const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
-    if (unit >= a.heads * groups) return;
     const int row0 = (unit % groups) * kUnitRows, r = blockIdx.y * 32 + lane;
-    if (row0 + static_cast<int>(blockIdx.y) * 32 >= R) return;
+    if (unit >= a.heads * groups || row0 + static_cast<int>(blockIdx.y) * 32 >= R) {
+        grid_dependency_wait();
+        return;
+    }
     int64_t before = 0, all = 0;
     for (int i = tid; i < a.B; i += kJoinThreads) {
         const int64_t n = tiles_of(a, i);
@@ -646,7 +696,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
     const int64_t per = (all + ctas - 1) / ctas;
     const int64_t u0 = before + int64_t(unit) * tiles;
     const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + tiles - 1) / per);
-    if (c0 == c1 || row0 + r >= R || r >= kUnitRows) return;
+    grid_dependency_wait();
+    if (c0 == c1 || row0 + r >= R || r >= kUnitRows || a.ok[b] == 0) return;
     float M = -INFINITY;
     for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * int64_t(c) + (c == c0)) * a.slot_rows + r].x);
     const float ref = M == -INFINITY ? 0.f : M;

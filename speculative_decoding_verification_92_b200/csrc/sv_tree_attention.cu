@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
     __shared__ int32_t up[2][SV_MAX_NODES];
     const int b = blockIdx.x, tid = threadIdx.x, N = a.N;
     grid_dependency_wait();
+    grid_launch_dependents();
     const int len = a.lens[b], count = a.counts ? a.counts[b] : N;
     const bool count_ok = count >= 0 && count <= N;
     const int64_t rows = int64_t(len) + count;
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
     const int words = a.heads * a.head_dim / 8;  // 16-byte words of a key row
     if (bad) {
         if (blockIdx.y == 0) {
-            if (tid == 0) a.rows[b] = 0;
+            if (tid == 0) a.ok[b] = 0;
             if (count_ok) {
                 const int per = a.q_heads * a.head_dim / 8;
                 const uint4 nan{Half<T>::kNan2, Half<T>::kNan2, Half<T>::kNan2, Half<T>::kNan2};
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
         if (tid < count)
             for (int w = 0; w < kMaskWords; ++w)
                 a.masks[(int64_t(b) * N + tid) * kMaskWords + w] = bits[cur][tid][w];
-        if (tid == 0) a.rows[b] = count > 0 ? static_cast<int>(rows) : 0;
+        if (tid == 0) a.ok[b] = 1;
     }
     // one warp per node
     const int lane = tid & 31, warps = gridDim.y * (kPrepThreads / 32);
@@ -132,7 +133,7 @@ sv_status attention_ok(const sv_tree_attention_shape* s, const sv_cache* c) {
 
 // The workspace: what the preparation finds, then the parts of cut units.
 struct AttnWorkspace {
-    size_t rows, masks, odd, ml, o, total;
+    size_t ok, masks, odd, ml, o, total;
     int slot_rows;
 };
 
@@ -142,7 +143,7 @@ AttnWorkspace workspace_layout(const sv_tree_attention_shape& s, const sv_cache&
     w.slot_rows = static_cast<int>(most < kUnitRows ? (most + 31) / 32 * 32 : kUnitRows);
     const size_t slots = 2 * size_t(kAttendMaxCtas) * w.slot_rows;
     size_t at = 0;
-    w.rows = at;  at += align256(size_t(s.B) * 4);
+    w.ok = at;  at += align256(size_t(s.B) * 4);
     w.masks = at; at += align256(size_t(s.B) * s.N * kMaskWords * 4);
     w.odd = at;   at += align256(size_t(s.B) * s.N * 4);
     w.ml = at;    at += align256(slots * sizeof(float2));
@@ -226,7 +227,7 @@ extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const s
                  s->k_stride_h * 2, s->v_stride_b * 2, s->v_stride_n * 2, s->v_stride_h * 2, s->o_stride_b * 2,
                  s->o_stride_n * 2, s->o_stride_h * 2, static_cast<const char*>(q), static_cast<const char*>(k),
                  static_cast<const char*>(v), static_cast<char*>(out), page_table, lens, parents, counts, scale,
-                 w.slot_rows, reinterpret_cast<int32_t*>(ws + w.rows), reinterpret_cast<uint32_t*>(ws + w.masks),
+                 w.slot_rows, reinterpret_cast<int32_t*>(ws + w.ok), reinterpret_cast<uint32_t*>(ws + w.masks),
                  reinterpret_cast<int32_t*>(ws + w.odd), reinterpret_cast<float2*>(ws + w.ml),
                  reinterpret_cast<float4*>(ws + w.o)};
     auto st = static_cast<cudaStream_t>(stream);

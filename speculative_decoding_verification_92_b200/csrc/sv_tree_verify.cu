@@ -280,7 +280,7 @@ __device__ __forceinline__ Part range_stats(const void* row, int lo, int hi, con
                     for (int k = 0; k < B::EV; ++k) {
                         double x, q;
                         exp2_table(y(static_cast<double>(z[k])), tab, &x, &q);
-                        s[k & 1] = fma(z[k] >= least ? x : 0.0, q, s[k & 1]);
+                        if (z[k] >= least) s[k & 1] = fma(x, q, s[k & 1]);  // (q is NaN for -inf)
                     }
                 };
                 if (near) add([&](double v) { return fma(v, c, -mc); });

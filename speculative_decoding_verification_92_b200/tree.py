@@ -10,9 +10,12 @@ idle slot).
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from . import _check, _dtype_code, _torch, library
-from .cache import _Cache, _cache, _ints, _on, _row_stride, _table
+import torch
+
+from . import BF16, F32, library
+from .cache import _bad_tensor, _cache, _call, _dense, _int_rows, _table
 
 __all__ = ["tree_attention", "tree_attention_workspace_bytes", "tree_verify", "MAX_NODES"]
 
@@ -22,22 +25,17 @@ _VP, _I32, _I64, _F32, _F64, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_in
                                     ctypes.c_size_t)
 
 
-class _TreeShape(ctypes.Structure):
-    _fields_ = [("B", _I32), ("N", _I32), ("V", _I32), ("dtype", _I32), ("row_stride", _I64)]
-
-
-class _AttentionShape(ctypes.Structure):
-    _fields_ = ([("B", _I32), ("N", _I32), ("q_heads", _I32), ("max_pages", _I32), ("table_stride", _I64)]
-                + [(f"{t}_stride_{d}", _I64) for t in "qkvo" for d in "bnh"])
-
-
+# sv_tree_shape: B, N, V, dtype, row_stride; sv_tree_attention_shape: B, N,
+# q_heads, max_pages, table_stride, strides of q, k, v and out.
+_TREE_SHAPE = struct.Struct("@4iq")
+_ATTENTION_SHAPE = struct.Struct("@4iq12q")
 _SIGNATURES = {
-    "sv_tree_attention_workspace_bytes": (_SZ, [ctypes.POINTER(_AttentionShape), ctypes.POINTER(_Cache)]),
-    "sv_tree_attention": (_I32, [ctypes.POINTER(_AttentionShape), ctypes.POINTER(_Cache), _VP, _VP, _VP, _VP, _VP,
-                                 _VP, _VP, _F32, _VP, _VP, _SZ, _VP]),
-    "sv_tree_verify": (_I32, [ctypes.POINTER(_TreeShape), _VP, _VP, _VP, _VP, _VP, _VP, _F64, _I32, _VP, _VP, _VP,
-                              _VP]),
+    "sv_tree_attention_workspace_bytes": (_SZ, [ctypes.c_char_p, ctypes.c_char_p]),
+    "sv_tree_attention": (_I32, [ctypes.c_char_p, ctypes.c_char_p, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _F32, _VP, _VP,
+                                 _SZ, _VP]),
+    "sv_tree_verify": (_I32, [ctypes.c_char_p, _VP, _VP, _VP, _VP, _VP, _VP, _F64, _I32, _VP, _VP, _VP, _VP]),
 }
+_LOGIT_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 _LIB = None
 
 
@@ -52,50 +50,36 @@ def _library():
     return _LIB
 
 
-def _logits(what, t, shape, device):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected the CUDA device of the call ({device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
-
-
 def _rows(what, t, shape, dtype, device):
     """Pointer of a [B, N, heads, head_dim] tensor with a contiguous last
     dimension, and its other strides (0 where there is one of a kind)."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must have the cache's dtype {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected the CUDA device of the call ({device})")
-    st = t.stride()
-    if st[3] != 1:
-        raise ValueError(f"{what} must have a contiguous last dimension")
-    return t.data_ptr(), [s if n > 1 else 0 for s, n in zip(st[:3], shape)]
+    s0, s1, s2, s3 = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if t.dtype == dtype and t.shape == shape and t.device == device and s3 == 1:
+        return t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0, s2 if shape[2] > 1 else 0
+    _bad_tensor(what, t, dtype, shape, device, "have a contiguous last dimension")
 
 
 def _attention_shapes(q, k, v, out, k_cache, v_cache, page_table):
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B, N, q_heads, head_dim], the caches [pages, page_size, heads, head_dim]")
-    B, N, Hq, D = q.shape
+    B, N, Hq, _ = q.shape
+    heads, D = k_cache.shape[2:]
     c = _cache(k_cache, v_cache)
     dt, dev = k_cache.dtype, k_cache.device
-    if tuple(page_table.shape[:1]) != (B,):
-        raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
-    (qp, qs), (kp, ks), (vp, vs), (op, os) = (
-        _rows("q", q, (B, N, Hq, c.head_dim), dt, dev), _rows("k", k, (B, N, c.heads, c.head_dim), dt, dev),
-        _rows("v", v, (B, N, c.heads, c.head_dim), dt, dev), _rows("out", out, q.shape, dt, dev))
-    _, max_pages = _table(page_table)
-    return c, _AttentionShape(B, N, Hq, max_pages, _row_stride(page_table), *qs, *ks, *vs, *os), (qp, kp, vp, op)
+    kv = (B, N, heads, D)
+    qp, *qs = _rows("q", q, (B, N, Hq, D), dt, dev)
+    kp, *ks = _rows("k", k, kv, dt, dev)
+    vp, *vs = _rows("v", v, kv, dt, dev)
+    op, *os = _rows("out", out, (B, N, Hq, D), dt, dev)
+    max_pages = _table(page_table)[1]
+    table, stride = _int_rows("page_table", page_table, (B, max_pages), dev)
+    return c, _ATTENTION_SHAPE.pack(B, N, Hq, max_pages, stride, *qs, *ks, *vs, *os), (qp, kp, vp, table), op
 
 
 def tree_attention_workspace_bytes(q, k, v, k_cache, v_cache, page_table) -> int:
     """Bytes of the workspace that tree_attention needs for these shapes."""
-    c, shape, _ = _attention_shapes(q, k, v, q, k_cache, v_cache, page_table)
-    return int(_library().sv_tree_attention_workspace_bytes(ctypes.byref(shape), ctypes.byref(c)))
+    c, shape, *_ = _attention_shapes(q, k, v, q, k_cache, v_cache, page_table)
+    return int(_library().sv_tree_attention_workspace_bytes(shape, c))
 
 
 def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, counts=None, *, scale=None, out=None,
@@ -113,23 +97,19 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     head_dim 64 and 128, page_size 16 to 128 (powers of two); a single new
     token per request is N = 1.  Calls that may run at the same time need
     separate workspaces."""
-    torch = _torch()
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    c, shape, (qp, kp, vp, op) = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
-    B, N, dev = shape.B, shape.N, k_cache.device
-    ints = (_ints("page_table", page_table, (B, shape.max_pages), dev, rows=True), _ints("lens", lens, (B,), dev),
-            _ints("parents", parents, (B, N), dev), _ints("counts", counts, (B,), dev))
+    c, shape, ptrs, op = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
+    B, N, dev = q.shape[0], q.shape[1], q.device
     lib = _library()
-    with _on(dev, stream) as st:
-        if workspace is None:
-            n = lib.sv_tree_attention_workspace_bytes(ctypes.byref(shape), ctypes.byref(c))
-            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        _check(lib.sv_tree_attention(ctypes.byref(shape), ctypes.byref(c), qp, kp, vp, *ints,
-                                     c.head_dim ** -0.5 if scale is None else float(scale), op, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), st), "sv_tree_attention")
+    if workspace is None:
+        n = lib.sv_tree_attention_workspace_bytes(shape, c)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _call(lib.sv_tree_attention, dev, stream, shape, c, *ptrs, _dense("lens", lens, torch.int32, (B,), dev),
+          _dense("parents", parents, torch.int32, (B, N), dev), _dense("counts", counts, torch.int32, (B,), dev),
+          k_cache.shape[3] ** -0.5 if scale is None else float(scale), op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -147,30 +127,24 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
     node 0 and the accepted nodes, then -1 (what ``cache_commit`` takes).  A
     request that is not valid gets -1 throughout.  Only rows on the accepted
     path are read; sums are held in 64 bits."""
-    torch = _torch()
     if target.dim() != 3:
         raise ValueError("target logits must be [B, N, row_stride]")
-    B, N, row_stride = target.shape
-    dev = target.device
-    if draft is not None and draft.dtype != target.dtype:
-        raise TypeError(f"draft logits must have the target's dtype {target.dtype}, got {draft.dtype}")
+    rows = target.shape
+    B, N, row_stride = rows
+    dev, dt = target.device, target.dtype
+    if dt not in _LOGIT_CODES:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dt}")
     if greedy:
         draft = uniforms = None
-    if uniforms is not None and uniforms.dtype != torch.float32:
-        raise TypeError(f"uniforms must be torch.float32, got {uniforms.dtype}")
-    shape = _TreeShape(B, N, row_stride if V is None else int(V), _dtype_code(target), row_stride)
-    ptrs = (_logits("target", target, (B, N, row_stride), dev),
-            None if draft is None else _logits("draft", draft, (B, N, row_stride), dev),
-            _ints("tokens", tokens, (B, N), dev), _ints("parents", parents, (B, N), dev),
-            _ints("counts", counts, (B,), dev),
-            None if uniforms is None else _logits("uniforms", uniforms, (B, N), dev))
-    lib = _library()
+    i32, nodes = torch.int32, (B, N)
+    shape = _TREE_SHAPE.pack(B, N, row_stride if V is None else int(V), _LOGIT_CODES[dt], row_stride)
     if out is None:
-        all_out = torch.empty(2 * B * N + B, dtype=torch.int32, device=dev)
-        out = all_out[2 * B * N:], all_out[:B * N].view(B, N), all_out[B * N:2 * B * N].view(B, N)
-    outs = (_ints("out accept_len", out[0], (B,), dev), _ints("out tokens", out[1], (B, N), dev),
-            _ints("out path", out[2], (B, N), dev))
-    with _on(dev, stream) as st:
-        _check(lib.sv_tree_verify(ctypes.byref(shape), *ptrs, float(temperature), int(bool(greedy)), *outs, st),
-               "sv_tree_verify")
+        out = (torch.empty(B, dtype=i32, device=dev), torch.empty(nodes, dtype=i32, device=dev),
+               torch.empty(nodes, dtype=i32, device=dev))
+    _call(_library().sv_tree_verify, dev, stream, shape, _dense("target", target, dt, rows, dev),
+          _dense("draft", draft, dt, rows, dev), _dense("tokens", tokens, i32, nodes, dev),
+          _dense("parents", parents, i32, nodes, dev), _dense("counts", counts, i32, (B,), dev),
+          _dense("uniforms", uniforms, torch.float32, nodes, dev), float(temperature), int(bool(greedy)),
+          _dense("out accept_len", out[0], i32, (B,), dev), _dense("out tokens", out[1], i32, nodes, dev),
+          _dense("out path", out[2], i32, nodes, dev))
     return out
