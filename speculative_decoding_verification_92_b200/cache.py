@@ -53,68 +53,77 @@ def _library():
     return _LIB
 
 
-def _bad_tensor(what, t, dtype, shape, device, layout):
+def _bad_tensor(what, t, dtype, shape, index, layout):
     """Raises what is wrong with a tensor that did not pass a quick check."""
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected the device of the call ({device})")
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, expected the device of the call (cuda:{index})")
     raise ValueError(f"{what} must {layout}")
 
 
-def _dense(what, t, dtype, shape, device):
-    """Pointer of a contiguous tensor of exactly this dtype, shape and device;
-    None passes through.  Calls of a few microseconds are checked here, so the
-    usual case is one expression."""
+def _cuda_index(what, t) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what} must be a CUDA tensor, got one on {t.device}")
+    return index
+
+
+def _dense(what, t, dtype, shape, index):
+    """Pointer of a contiguous tensor of exactly this dtype, shape and CUDA
+    device; None passes through.  Calls of a few microseconds are checked
+    here, so the usual case is one expression."""
     if t is None:
         return None
-    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype == dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
-    _bad_tensor(what, t, dtype, shape, device, "be contiguous")
+    _bad_tensor(what, t, dtype, shape, index, "be contiguous")
 
 
-def _int_rows(what, t, shape, device):
+def _int_rows(what, t, shape, index):
     """Pointer and row stride of an int32 matrix with contiguous rows."""
-    if t.dtype == torch.int32 and t.shape == shape and t.device == device:
+    if t.dtype == torch.int32 and t.shape == shape and t.get_device() == index:
         s0, s1 = t.stride()
         if s1 == 1 or shape[1] <= 1:
             if shape[0] <= 1:
                 return t.data_ptr(), shape[1]
             if s0 >= shape[1]:
                 return t.data_ptr(), s0
-    _bad_tensor(what, t, torch.int32, shape, device, "have contiguous rows that do not overlap")
+    _bad_tensor(what, t, torch.int32, shape, index, "have contiguous rows that do not overlap")
 
 
-def _cache(k, v) -> bytes:
+def _cache(k, v, index) -> bytes:
     """The C description of a cache; 4-d tensors are one layer."""
     shape, st, dtype = k.shape, k.stride(), k.dtype
-    if (len(shape) not in (4, 5) or v.shape != shape or v.dtype != dtype or v.device != k.device
-            or v.stride() != st or (st[-1] != 1 and shape[-1] > 1)):
+    if (len(shape) not in (4, 5) or v.shape != shape or v.dtype != dtype or v.stride() != st
+            or (st[-1] != 1 and shape[-1] > 1)):
         raise ValueError("k_cache and v_cache must be [layers, pages, page_size, heads, head_dim] tensors of one "
-                         "shape, dtype, device and layout with a contiguous last dimension")
+                         "shape, dtype and layout with a contiguous last dimension")
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"the caches are on {k.device} and {v.device}, expected the device of the call (cuda:{index})")
     if dtype not in _KV_CODES:
         raise TypeError(f"the cache must be float32, bfloat16 or float16, got {dtype}")
     if len(shape) == 4:
-        shape, st = (1, *shape), (0, *st)
-    s0, s1, s2, s3, _ = st
-    n0, n1, n2, n3, n4 = shape
+        n1, n2, n3, n4 = shape
+        s1, s2, s3, _ = st
+        n0, s0 = 1, 0
+    else:
+        n0, n1, n2, n3, n4 = shape
+        s0, s1, s2, s3, _ = st
     return _CACHE.pack(k.data_ptr(), v.data_ptr(), n0, n1, n2, n3, n4, _KV_CODES[dtype], s0 if n0 > 1 else 0,
                        s1 if n1 > 1 else 0, s2 if n2 > 1 else 0, s3 if n3 > 1 else 0)
 
 
-def _call(fn, device, stream, *args):
-    """The C call with the tensors' device current, on `stream` or the device's
+def _call(fn, index, stream, *args):
+    """The C call with device `index` current, on `stream` or the device's
     current stream."""
-    index = device.index
-    if index is None:
-        raise ValueError(f"{fn.__name__} needs CUDA tensors, got tensors on {device}")
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch._C._cuda_getDevice():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, handle)
     if status:
         raise SpecVerifyError(status, fn.__name__)
@@ -134,9 +143,9 @@ def cache_resize(page_table, lens, refcount, page_size, *, status=None, stream=N
     0, or -1 where the slot was left unchanged (its length or entries are not
     valid, or the free pages did not reach it)."""
     slots, max_pages = _table(page_table)
-    dev = page_table.device
+    dev = _cuda_index("page_table", page_table)
     if status is None:
-        status = torch.empty(slots, dtype=torch.int32, device=dev)
+        status = torch.empty(slots, dtype=torch.int32, device=page_table.device)
     pages = refcount.shape
     if len(pages) != 1:
         raise ValueError("refcount must be [pages]")
@@ -155,14 +164,12 @@ def cache_commit(k_cache, v_cache, page_table, lens, path, *, out_lens=None, str
     the new lengths ``lens + n`` (int32, -1 for a request that is not valid and
     was left alone); ``out_lens`` must be another tensor than ``lens``."""
     B, max_pages = _table(page_table)
-    dev = page_table.device
-    c = _cache(k_cache, v_cache)
+    dev = _cuda_index("page_table", page_table)
+    c = _cache(k_cache, v_cache, dev)
     if out_lens is None:
-        out_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        out_lens = torch.empty(B, dtype=torch.int32, device=page_table.device)
     if path.dim() != 2:
         raise ValueError("path must be [B, width]")
-    if k_cache.device != dev:
-        raise ValueError(f"the cache is on {k_cache.device}, page_table on {dev}")
     width = path.shape[1]
     table, stride = _int_rows("page_table", page_table, (B, max_pages), dev)
     rows, path_stride = _int_rows("path", path, (B, width), dev)
@@ -179,15 +186,13 @@ def cache_fork(k_cache, v_cache, page_table, lens, refcount, src, dst, *, status
     ``refcount`` in place; returns int32 ``status [forks]``: 0, -1 (not valid,
     nothing changed) or -2 (no free page left: ``dst`` is left empty)."""
     slots, max_pages = _table(page_table)
-    dev = page_table.device
-    c = _cache(k_cache, v_cache)
+    dev = _cuda_index("page_table", page_table)
+    c = _cache(k_cache, v_cache, dev)
     if src.dim() != 1:
         raise ValueError("src must be [forks]")
-    if k_cache.device != dev:
-        raise ValueError(f"the cache is on {k_cache.device}, page_table on {dev}")
     n = src.shape[0]
     if status is None:
-        status = torch.empty(n, dtype=torch.int32, device=dev)
+        status = torch.empty(n, dtype=torch.int32, device=page_table.device)
     table, stride = _int_rows("page_table", page_table, (slots, max_pages), dev)
     pages = k_cache.shape[-4]
     _call(_library().sv_cache_fork, dev, stream, c, table, stride, slots, max_pages,

@@ -4,12 +4,12 @@
 // Mathematics.  For one request and key/value head, the rows of Q are its
 // (node, query head of the group) pairs, up to 256 per unit of work, in tiles
 // of 128.  Per tile of 128 cached rows: S = Q K^T, p = 2^(S c - m) with m a
-// running reference of each row (its maximum so far, or up to 2^8 below it),
-// O += P V, l += sum p.  O and l are rescaled only when the maximum rises by
-// more than 2^8 over the reference: p then stays below 2^8, far from
-// overflow, and most tiles need no pass over O.  p is rounded to the cache's
-// type for the second product; l sums the rounded values, so that the weights
-// of a row sum to one exactly as they are applied.
+// reference of each row (its maximum over the first tile of its run),
+// O += P V, l += sum p.  The exponents' range leaves room above the reference
+// and a weight's relative error does not depend on it, so the maximum is not
+// followed: only when a tile's weights come to more than 2^15 is a new one
+// looked for and O and l rescaled.  p is rounded to the cache's type for the
+// second product.
 //
 // Roles (10 warps).  Warps 0-3 and 4-7 are two softmax groups, a thread per
 // row of S (a lane of tensor memory).  Warp 8 loads K and V tiles by TMA, one
@@ -80,30 +80,61 @@ struct Half;
 template <>
 struct Half<__nv_bfloat16> {
     static constexpr uint32_t kNan2 = 0x7fc07fc0u, kExp2 = 0x7f807f80u, kType = 1;
+    static constexpr int kExp2Degree = 3;
     static constexpr float kShift = 0.f;
     __device__ static uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    __device__ static uint64_t widen(uint32_t w) { return bf16x2_to_f2(w); }
 };
 template <>
 struct Half<__half> {
     static constexpr uint32_t kNan2 = 0x7e007e00u, kExp2 = 0x7c007c00u, kType = 0;
+    static constexpr int kExp2Degree = 4;
     // weights are kept 2^6 up, so that small ones do not fall among the
-    // subnormals of a type whose least normal is 2^-14 (2^(6 + 8) < 65504)
+    // subnormals of a type whose least normal is 2^-14; 128 of them come to 2^13
     static constexpr float kShift = 6.f;
     __device__ static uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    __device__ static uint64_t widen(uint32_t w) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        return f2_pack(f.x, f.y);
-    }
 };
+
+// 2^x for a pair on the multiply-add pipe: 2^n 2^f with n the nearest whole
+// number and a minimax polynomial for 2^f on [-1/2, 1/2], relative error 7.5e-5
+// (degree 3) or 2.6e-6 (degree 4), well inside half a step of the type that
+// the weights are rounded to.  The special-function unit does 16 a cycle and
+// is the softmax's bottleneck; kExp2Every says which pairs it is spared.
+constexpr int kExp2Every = 4;
+// What 128 weights may come to before their row gets a new reference: within
+// the range of fp16, and far from where the products could overflow.
+constexpr float kMostSum = 32768.f;
+template <int kDegree>
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    x = f2_pack(max_nan(a, -126.f), max_nan(b, -126.f));  // below: 2^-126, nothing beside a row's largest weight
+    const uint64_t t = f2_add(x, f2_pack(12582912.f, 12582912.f));  // 1.5 2^23: the low bits are n
+    const uint64_t f = f2_fma(f2_add(t, f2_pack(-12582912.f, -12582912.f)), f2_pack(-1.f, -1.f), x);
+    uint64_t p;
+    if constexpr (kDegree == 3) {
+        p = f2_fma(f2_pack(0.0551716685f, 0.0551716685f), f, f2_pack(0.2426111251f, 0.2426111251f));
+        p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
+        p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
+    } else {
+        p = f2_fma(f2_pack(0.0095701021f, 0.0095701021f), f, f2_pack(0.0559178591f, 0.0559178591f));
+        p = f2_fma(p, f, f2_pack(0.2402474433f, 0.2402474433f));
+        p = f2_fma(p, f, f2_pack(0.6931217909f, 0.6931217909f));
+        p = f2_fma(p, f, f2_pack(0.9999992847f, 0.9999992847f));
+    }
+    float pa, pb, ta, tb;
+    f2_unpack(p, pa, pb);
+    f2_unpack(t, ta, tb);
+    return f2_pack(__uint_as_float(__float_as_uint(pa) + (__float_as_uint(ta) << 23)),
+                   __uint_as_float(__float_as_uint(pb) + (__float_as_uint(tb) << 23)));
+}
 
 // ---------------------------------------------------------------------------
 // The line of tiles.
@@ -218,6 +249,74 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* mask, int a0) {
     return __funnelshift_r(mask[w], w + 1 < kMaskWords ? mask[w + 1] : 0u, s);
 }
 
+template <bool kMasked>
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t see) {
+    if (kMasked) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (!(see >> k & 1u)) s[k] = 0xff800000u;
+    }
+}
+
+// Maximum of this row's 128 scores at `addr`, among those it sees.
+template <bool kMasked>
+__device__ __forceinline__ float tile_top(uint32_t addr, const uint32_t (&see)[4]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t s[32];
+        tmem_load(s, addr + 32 * w);
+        hide<kMasked>(s, see[w]);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) m[k / 2 & 3] = max3(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), m[k / 2 & 3]);
+    }
+    return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+
+// Weights 2^(s c - ref) of the row's 128 scores, packed in pairs; returns
+// their sum (NaN or past kMostSum where the reference is too low for the type
+// to hold them).  The next 32 scores are on their way while 32 are worked on,
+// and nothing branches in between, so that the pairs overlap in the pipes.
+template <typename T, bool kMasked>
+__device__ __forceinline__ float tile_weights(uint32_t addr, const uint32_t (&see)[4], float c, float ref,
+                                              uint32_t (&packed)[64]) {
+    using H = Half<T>;
+    const uint64_t cc = f2_pack(c, c), mm = f2_pack(-ref, -ref);
+    uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+    float top = -INFINITY;  // of the exponents that exp2_pair takes
+    uint32_t s[2][32];
+    tmem_start(s[0], addr);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        tmem_arrived(s[w & 1]);
+        if (w < 3) tmem_start(s[(w + 1) & 1], addr + 32 * (w + 1));
+        uint32_t(&v)[32] = s[w & 1];
+        hide<kMasked>(v, see[w]);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, mm);
+            float x, y;
+            f2_unpack(x2, x, y);
+            if (k / 2 % kExp2Every == kExp2Every - 1) {
+                top = max3(x, y, top);
+                f2_unpack(exp2_pair<H::kExp2Degree>(x2), x, y);
+                if (kMasked) {  // what is not seen weighs exactly nothing
+                    x = see[w] >> k & 1u ? x : 0.f;
+                    y = see[w] >> (k + 1) & 1u ? y : 0.f;
+                }
+            } else {
+                x = ex2_approx(x);
+                y = ex2_approx(y);
+            }
+            packed[16 * w + k / 2] = H::pack(x, y);
+            sum[k / 2 & 1] = f2_add(sum[k / 2 & 1], f2_pack(x, y));
+        }
+    }
+    float x, y;
+    f2_unpack(f2_add(sum[0], sum[1]), x, y);
+    return top > 64.f ? INFINITY : x + y;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads, 1)
 tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
@@ -293,40 +392,58 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     Piece p{};
 
     if (warp == 8) {
-        // ---- loads: lane i has box i of a tile, 64 columns of a page
-        constexpr int kHalves = D / 64;
-        uint32_t kn = 0, vn = 0;  // tiles issued
+        // ---- loads: a box per page and 64 columns
+        constexpr int kPages = kTile / 16;  // pages of a tile, at most
+        uint32_t kn = 0, vn = 0;            // tiles issued
         bool ok = true;
         const int per_tile = kTile / a.page_size;
-        const int page = lane / kHalves, x = lane % kHalves;
-        const uint32_t to = x * (kTile * 128) + page * a.page_size * 128;
         auto wait_new_rows = [] {
             grid_dependency_wait();
             asm volatile("fence.proxy.async;" ::: "memory");
         };
-        // the page id of this lane's box in a tile (-1: none)
-        auto page_id = [&](int tile) {
-            const int at = tile * per_tile + page;
-            return page < per_tile && at * a.page_size < p.rows ? a.table[p.b * a.table_stride + at] : -1;
+        struct Ids {
+            int id[kPages];  // -1: past the request
+        };
+        auto fetch = [&](int tile) {
+            Ids x;
+            const int32_t* ids = a.table + p.b * a.table_stride + tile * per_tile;
+#pragma unroll
+            for (int i = 0; i < kPages; ++i)
+                x.id[i] = i < per_tile && (tile * per_tile + i) * a.page_size < p.rows ? ids[i] : -1;
+            return x;
         };
         auto load = [&](const CUtensorMap* map, unsigned char* ring, uint64_t* full, uint64_t* empty, uint32_t stages,
-                        uint32_t& n, int id) {
+                        uint32_t& n, const Ids& ids) {
             const uint32_t s = n % stages;
             ok = ok && (n < stages || mbar_wait_bounded(empty + s, (n / stages - 1) & 1, kAttendTimeoutNs));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            const int boxes = __popc(__ballot_sync(0xffffffffu, id >= 0));
-            if (lane == 0) mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(boxes * a.page_size * 128));
+            unsigned char* dst = ring + s * TB;
+            if (elect_one()) {
+                int pages = 0;
+#pragma unroll
+                for (int i = 0; i < kPages; ++i) pages += ids.id[i] >= 0;
+                mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(pages * a.page_size * D * 2));
+#pragma unroll
+                for (int i = 0; i < kPages; ++i)
+                    if (ids.id[i] >= 0) {
+#pragma unroll
+                        for (int x = 0; x < D; x += 64)
+                            tma_load_4d(dst + (x / 64) * (kTile * 128) + i * a.page_size * 128, map, x, p.head, 0,
+                                        ids.id[i], full + s);
+                    }
+            }
             __syncwarp();
-            if (id >= 0) tma_load_4d(ring + s * TB + to, map, x * 64, p.head, 0, id, full + s);
             ++n;
         };
         while (ok && it.next(a, p)) {
-            int id = page_id(p.first), next = p.n > 1 ? page_id(p.first + 1) : -1;
+            Ids id = fetch(p.first), next = id;
+            if (p.n > 1) next = fetch(p.first + 1);
             if (reads_new_rows(p, p.first)) wait_new_rows();
             load(&kmap, ks, ctl.kfull, ctl.kempty, KS, kn, id);
             for (int i = 0; i < p.n && ok; ++i) {
-                const int after = i + 2 < p.n ? page_id(p.first + i + 2) : -1;
+                Ids after = next;
+                if (i + 2 < p.n) after = fetch(p.first + i + 2);
                 if (i + 1 < p.n) {
                     if (reads_new_rows(p, p.first + i + 1)) wait_new_rows();
                     load(&kmap, ks, ctl.kfull, ctl.kempty, KS, kn, next);
@@ -345,34 +462,47 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
         }
     } else if (warp == 9) {
         // ---- matrix products
-        if (lane == 0) {
+        {
             uint32_t kn = 0, vn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
             bool ok = true;
             const uint32_t qaddr = smem_u32(qs), kaddr = smem_u32(ks), vaddr = smem_u32(vs);
             auto wait = [&](uint64_t* bar, uint32_t n) {
                 ok = ok && mbar_wait_bounded(bar, n & 1, kAttendTimeoutNs);
-                if (ok) tcgen05_fence_after();
+                ok = __all_sync(0xffffffffu, ok);
+                tcgen05_fence_after();
             };
+            // (advancing an operand adds to its address field, in units of 16 bytes)
             auto qk = [&](int t, int qtile) {  // S[t] = Q[qtile] K^T, K the tile `kn`
-                const uint32_t k0 = kaddr + (kn % KS) * TB, q0 = qaddr + qtile * TB;
+                const uint64_t q0 = smem_operand(qaddr + qtile * TB, 16, 1024);
+                const uint64_t k0 = smem_operand(kaddr + (kn % KS) * TB, 16, 1024);
+                const uint32_t d = tmem + s_at(t);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < D; x += 16) {
-                    const uint32_t at = (x / 64) * (kTile * 128) + (x % 64) * 2;
-                    mma_ss(tmem + s_at(t), smem_operand(q0 + at, 16, 1024), smem_operand(k0 + at, 16, 1024),
-                           mma_shape(H::kType, kTile, false), x > 0);
+                    for (int x = 0; x < D; x += 16) {
+                        const uint32_t at = ((x / 64) * (kTile * 128) + (x % 64) * 2) >> 4;
+                        mma_ss(d, q0 + at, k0 + at, mma_shape(H::kType, kTile, false), x > 0);
+                    }
+                    tcgen05_commit(&ctl.sfull[t]);
                 }
-                tcgen05_commit(&ctl.sfull[t]);
+                __syncwarp();
             };
             auto pv = [&](int t, bool add) {  // O[t] (+)= P[t] V, V the tile `vn`
-                const uint32_t v0 = vaddr + (vn % VS) * TB;
+                const uint64_t v0 = smem_operand(vaddr + (vn % VS) * TB, kTile * 128, 1024);
+                const uint32_t d = tmem + o_at(t), w = tmem + s_at(t);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < kTile; x += 16)
-                    mma_ts(tmem + o_at(t), tmem + s_at(t) + x / 2, smem_operand(v0 + x * 128, kTile * 128, 1024),
-                           mma_shape(H::kType, D, true), add || x > 0);
+                    for (int x = 0; x < kTile; x += 16)
+                        mma_ts(d, w + x / 2, v0 + (x * 128 >> 4), mma_shape(H::kType, D, true), add || x > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) tcgen05_commit(bar);
+                __syncwarp();
             };
             auto k_ready = [&] { wait(&ctl.kfull[kn % KS], kn / KS); };
             auto k_done = [&] {
-                tcgen05_commit(&ctl.kempty[kn % KS]);
+                commit(&ctl.kempty[kn % KS]);
                 ++kn;
             };
             while (ok && it.next(a, p)) {
@@ -392,9 +522,9 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                         wait(&ctl.pfull[t], pn[t]++);
                         if (!ok) break;
                         pv(t, i >= 2);
-                        tcgen05_commit(&ctl.vempty[vn % VS]);
+                        commit(&ctl.vempty[vn % VS]);
                         ++vn;
-                        if (i + 2 >= p.n) tcgen05_commit(&ctl.ofull[t]);
+                        if (i + 2 >= p.n) commit(&ctl.ofull[t]);
                         if (i + 2 < p.n) {
                             k_ready();
                             if (!ok) break;
@@ -406,9 +536,9 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                             wait(&ctl.pfull[t], pn[t]++);
                             if (!ok) break;
                             pv(t, i > 0);
-                            if (t == 1) tcgen05_commit(&ctl.vempty[vn % VS]);
+                            if (t == 1) commit(&ctl.vempty[vn % VS]);
                             if (i + 1 == p.n) {
-                                tcgen05_commit(&ctl.ofull[t]);
+                                commit(&ctl.ofull[t]);
                             } else {
                                 if (t == 0) k_ready();
                                 if (!ok) break;
@@ -503,26 +633,24 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                             odd |= (see[w] & ctl.odd[t][parity][w]) != 0;
                         }
                     }
-                    // the scores are read twice, for the maximum and for the weights: tensor
-                    // memory is faster than 128 registers are cheap
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int w = 0; w < 4; w += 2) {
-                        uint32_t s[64];
-                        tmem_load(s, lanes + s_at(t) + 32 * w);
-                        if (tail) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (!(see[w + k / 32] >> (k % 32) & 1u)) s[k] = 0xff800000u;
+                    // Weights against the reference so far; only where some row of the warp rises
+                    // too far over it for its weights to be held (and in the first tile of a
+                    // piece) is the maximum looked for and the reference moved there.
+                    uint32_t packed[64];
+                    float part = 0.f;
+                    bool fresh = __any_sync(0xffffffffu, m == -INFINITY);  // a row without a reference
+                    for (;;) {
+                        const float ref = m == -INFINITY ? 0.f : m;  // a row that sees nothing yet: all weights 0
+                        if (!fresh) {
+                            part = tail ? tile_weights<T, true>(lanes + s_at(t), see, c, ref, packed)
+                                        : tile_weights<T, false>(lanes + s_at(t), see, c, ref, packed);
+                            // (a sum that is NaN is not mended by another reference)
+                            if (!__any_sync(0xffffffffu, part > kMostSum)) break;
                         }
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            m4[k / 2 & 3] = max3(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), m4[k / 2 & 3]);
-                    }
-                    const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * c - H::kShift;
-                    const bool rise = i == from ? top > m : top > m + 8.f;
-                    if (__any_sync(0xffffffffu, rise)) {
-                        const float f = top > m ? ex2_approx(m - top) : 1.f;   // 0 where there was nothing yet
+                        const float best = tail ? tile_top<true>(lanes + s_at(t), see) : tile_top<false>(lanes + s_at(t), see);
+                        const float top = best * c - H::kShift;
+                        if (!fresh && !__any_sync(0xffffffffu, top > m)) break;
+                        const float f = top > m ? ex2_approx(m - top) : 1.f;  // 0 where there was nothing yet
                         if (top > m) m = top;
                         if (i != from) {
                             l *= f;
@@ -535,32 +663,17 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                                 tmem_store(lanes + o_at(t) + x, o);
                             }
                         }
+                        fresh = false;
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;  // a row that sees nothing here: all weights 0
-                    const uint64_t cc = f2_pack(c, c), mm = f2_pack(-ref, -ref);
-                    uint64_t sum = f2_pack(0.f, 0.f);
-                    // (the weights of columns 32 w .. go over scores that have been read)
+                    l += part;
+                    // the weights go over the scores
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        uint32_t s[32], packed[16];
-                        tmem_load(s, lanes + s_at(t) + 32 * w);
-                        if (tail) {
+                        uint32_t s[16];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(see[w] >> k & 1u)) s[k] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float x, y;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, mm), x, y);
-                            packed[k / 2] = H::pack(ex2_approx(x), ex2_approx(y));
-                            sum = f2_add(sum, H::widen(packed[k / 2]));
-                        }
-                        tmem_store(lanes + s_at(t) + 16 * w, packed);
+                        for (int k = 0; k < 16; ++k) s[k] = packed[16 * w + k];
+                        tmem_store(lanes + s_at(t) + 16 * w, s);
                     }
-                    float sx, sy;
-                    f2_unpack(sum, sx, sy);
-                    l += sx + sy;
                     tmem_wait_st();
                 }
                 tcgen05_fence_before();

@@ -15,7 +15,7 @@ import struct
 import torch
 
 from . import BF16, F32, library
-from .cache import _bad_tensor, _cache, _call, _dense, _int_rows, _table
+from .cache import _bad_tensor, _cache, _call, _cuda_index, _dense, _int_rows, _table
 
 __all__ = ["tree_attention", "tree_attention_workspace_bytes", "tree_verify", "MAX_NODES"]
 
@@ -50,13 +50,13 @@ def _library():
     return _LIB
 
 
-def _rows(what, t, shape, dtype, device):
+def _rows(what, t, shape, dtype, index):
     """Pointer of a [B, N, heads, head_dim] tensor with a contiguous last
     dimension, and its other strides (0 where there is one of a kind)."""
     s0, s1, s2, s3 = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
-    if t.dtype == dtype and t.shape == shape and t.device == device and s3 == 1:
+    if t.dtype == dtype and t.shape == shape and t.get_device() == index and s3 == 1:
         return t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0, s2 if shape[2] > 1 else 0
-    _bad_tensor(what, t, dtype, shape, device, "have a contiguous last dimension")
+    _bad_tensor(what, t, dtype, shape, index, "have a contiguous last dimension")
 
 
 def _attention_shapes(q, k, v, out, k_cache, v_cache, page_table):
@@ -64,8 +64,8 @@ def _attention_shapes(q, k, v, out, k_cache, v_cache, page_table):
         raise ValueError("q must be [B, N, q_heads, head_dim], the caches [pages, page_size, heads, head_dim]")
     B, N, Hq, _ = q.shape
     heads, D = k_cache.shape[2:]
-    c = _cache(k_cache, v_cache)
-    dt, dev = k_cache.dtype, k_cache.device
+    dt, dev = k_cache.dtype, _cuda_index("k_cache", k_cache)
+    c = _cache(k_cache, v_cache, dev)
     kv = (B, N, heads, D)
     qp, *qs = _rows("q", q, (B, N, Hq, D), dt, dev)
     kp, *ks = _rows("k", k, kv, dt, dev)
@@ -100,13 +100,13 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     c, shape, ptrs, op = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
-    B, N, dev = q.shape[0], q.shape[1], q.device
+    B, N, dev = q.shape[0], q.shape[1], q.get_device()
     lib = _library()
     if workspace is None:
         n = lib.sv_tree_attention_workspace_bytes(shape, c)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
     _call(lib.sv_tree_attention, dev, stream, shape, c, *ptrs, _dense("lens", lens, torch.int32, (B,), dev),
           _dense("parents", parents, torch.int32, (B, N), dev), _dense("counts", counts, torch.int32, (B,), dev),
           k_cache.shape[3] ** -0.5 if scale is None else float(scale), op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -131,20 +131,24 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
         raise ValueError("target logits must be [B, N, row_stride]")
     rows = target.shape
     B, N, row_stride = rows
-    dev, dt = target.device, target.dtype
+    dev, dt = _cuda_index("target", target), target.dtype
     if dt not in _LOGIT_CODES:
         raise TypeError(f"logits must be float32 or bfloat16, got {dt}")
     if greedy:
         draft = uniforms = None
     i32, nodes = torch.int32, (B, N)
-    shape = _TREE_SHAPE.pack(B, N, row_stride if V is None else int(V), _LOGIT_CODES[dt], row_stride)
     if out is None:
-        out = (torch.empty(B, dtype=i32, device=dev), torch.empty(nodes, dtype=i32, device=dev),
-               torch.empty(nodes, dtype=i32, device=dev))
-    _call(_library().sv_tree_verify, dev, stream, shape, _dense("target", target, dt, rows, dev),
-          _dense("draft", draft, dt, rows, dev), _dense("tokens", tokens, i32, nodes, dev),
-          _dense("parents", parents, i32, nodes, dev), _dense("counts", counts, i32, (B,), dev),
-          _dense("uniforms", uniforms, torch.float32, nodes, dev), float(temperature), int(bool(greedy)),
-          _dense("out accept_len", out[0], i32, (B,), dev), _dense("out tokens", out[1], i32, nodes, dev),
-          _dense("out path", out[2], i32, nodes, dev))
+        at = target.device
+        out = (torch.empty(B, dtype=i32, device=at), torch.empty(nodes, dtype=i32, device=at),
+               torch.empty(nodes, dtype=i32, device=at))
+        outs = [x.data_ptr() for x in out]
+    else:
+        outs = (_dense("out accept_len", out[0], i32, (B,), dev), _dense("out tokens", out[1], i32, nodes, dev),
+                _dense("out path", out[2], i32, nodes, dev))
+    _call(_library().sv_tree_verify, dev, stream,
+          _TREE_SHAPE.pack(B, N, row_stride if V is None else int(V), _LOGIT_CODES[dt], row_stride),
+          _dense("target", target, dt, rows, dev), _dense("draft", draft, dt, rows, dev),
+          _dense("tokens", tokens, i32, nodes, dev), _dense("parents", parents, i32, nodes, dev),
+          _dense("counts", counts, i32, (B,), dev), _dense("uniforms", uniforms, torch.float32, nodes, dev),
+          float(temperature), int(bool(greedy)), *outs)
     return out
