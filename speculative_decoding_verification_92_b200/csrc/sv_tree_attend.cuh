@@ -48,7 +48,6 @@ constexpr int kUnitRows = 2 * kTile;            // rows of Q per unit of work
 constexpr int kMaskWords = SV_MAX_NODES / 32;
 constexpr int kAttendThreads = 320;
 constexpr int kAttendMaxCtas = 160;
-constexpr uint64_t kAttendTimeoutNs = 2000000000ull;
 
 struct AttnParams {
     char* kc;
@@ -103,10 +102,12 @@ struct Half<__half> {
 };
 
 // 2^x for a pair on the multiply-add pipe: 2^n 2^f with n the nearest whole
-// number and a minimax polynomial for 2^f on [-1/2, 1/2], relative error 7.5e-5
-// (degree 3) or 2.6e-6 (degree 4), well inside half a step of the type that
-// the weights are rounded to.  The special-function unit does 16 a cycle and
-// is the softmax's bottleneck; kExp2Every says which pairs it is spared.
+// number and a minimax polynomial for 2^f on [-1/2, 1/2] that is 1 at 0,
+// relative error 1.0e-04 (degree 3) or 2.8e-06 (degree 4), well inside half a step of
+// the type that the weights are rounded to.  Below -127 it is exactly 0: there
+// n = -127 takes the exponent of 1 to nothing.  The special-function unit does
+// 16 a cycle and is the softmax's bottleneck; kExp2Every says which pairs it is
+// spared.
 constexpr int kExp2Every = 4;
 // What 128 weights may come to before their row gets a new reference: within
 // the range of fp16, and far from where the products could overflow.
@@ -115,19 +116,19 @@ template <int kDegree>
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
     float a, b;
     f2_unpack(x, a, b);
-    x = f2_pack(max_nan(a, -126.f), max_nan(b, -126.f));  // below: 2^-126, nothing beside a row's largest weight
+    x = f2_pack(max_nan(a, -127.f), max_nan(b, -127.f));
     const uint64_t t = f2_add(x, f2_pack(12582912.f, 12582912.f));  // 1.5 2^23: the low bits are n
     const uint64_t f = f2_fma(f2_add(t, f2_pack(-12582912.f, -12582912.f)), f2_pack(-1.f, -1.f), x);
     uint64_t p;
     if constexpr (kDegree == 3) {
-        p = f2_fma(f2_pack(0.0551716685f, 0.0551716685f), f, f2_pack(0.2426111251f, 0.2426111251f));
-        p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
-        p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
+        p = f2_fma(f2_pack(0.05500893085f, 0.05500893085f), f, f2_pack(0.2422109594f, 0.2422109594f));
+        p = f2_fma(p, f, f2_pack(0.6932829272f, 0.6932829272f));
+        p = f2_fma(p, f, f2_pack(1.f, 1.f));
     } else {
-        p = f2_fma(f2_pack(0.0095701021f, 0.0095701021f), f, f2_pack(0.0559178591f, 0.0559178591f));
-        p = f2_fma(p, f, f2_pack(0.2402474433f, 0.2402474433f));
-        p = f2_fma(p, f, f2_pack(0.6931217909f, 0.6931217909f));
-        p = f2_fma(p, f, f2_pack(0.9999992847f, 0.9999992847f));
+        p = f2_fma(f2_pack(0.00958285307f, 0.00958285307f), f, f2_pack(0.05590642463f, 0.05590642463f));
+        p = f2_fma(p, f, f2_pack(0.2402409861f, 0.2402409861f));
+        p = f2_fma(p, f, f2_pack(0.6931241934f, 0.6931241934f));
+        p = f2_fma(p, f, f2_pack(1.f, 1.f));
     }
     float pa, pb, ta, tb;
     f2_unpack(p, pa, pb);
@@ -249,37 +250,25 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* mask, int a0) {
     return __funnelshift_r(mask[w], w + 1 < kMaskWords ? mask[w + 1] : 0u, s);
 }
 
-template <bool kMasked>
-__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t see) {
-    if (kMasked) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            if (!(see >> k & 1u)) s[k] = 0xff800000u;
-    }
-}
-
-// Maximum of this row's 128 scores at `addr`, among those it sees.
-template <bool kMasked>
-__device__ __forceinline__ float tile_top(uint32_t addr, const uint32_t (&see)[4]) {
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+// Maximum of this row's 128 scores at `addr`.
+__device__ __forceinline__ float tile_top(uint32_t addr) {
+    float m = -INFINITY;
+#pragma unroll 1
     for (int w = 0; w < 4; ++w) {
         uint32_t s[32];
         tmem_load(s, addr + 32 * w);
-        hide<kMasked>(s, see[w]);
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) m[k / 2 & 3] = max3(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), m[k / 2 & 3]);
+        for (int k = 0; k < 32; k += 2) m = max3(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), m);
     }
-    return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+    return m;
 }
 
 // Weights 2^(s c - ref) of the row's 128 scores, packed in pairs; returns
 // their sum (NaN or past kMostSum where the reference is too low for the type
 // to hold them).  The next 32 scores are on their way while 32 are worked on,
 // and nothing branches in between, so that the pairs overlap in the pipes.
-template <typename T, bool kMasked>
-__device__ __forceinline__ float tile_weights(uint32_t addr, const uint32_t (&see)[4], float c, float ref,
-                                              uint32_t (&packed)[64]) {
+template <typename T>
+__device__ __forceinline__ float tile_weights(uint32_t addr, float c, float ref, uint32_t (&packed)[64]) {
     using H = Half<T>;
     const uint64_t cc = f2_pack(c, c), mm = f2_pack(-ref, -ref);
     uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -291,7 +280,6 @@ __device__ __forceinline__ float tile_weights(uint32_t addr, const uint32_t (&se
         tmem_arrived(s[w & 1]);
         if (w < 3) tmem_start(s[(w + 1) & 1], addr + 32 * (w + 1));
         uint32_t(&v)[32] = s[w & 1];
-        hide<kMasked>(v, see[w]);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, mm);
@@ -300,10 +288,6 @@ __device__ __forceinline__ float tile_weights(uint32_t addr, const uint32_t (&se
             if (k / 2 % kExp2Every == kExp2Every - 1) {
                 top = max3(x, y, top);
                 f2_unpack(exp2_pair<H::kExp2Degree>(x2), x, y);
-                if (kMasked) {  // what is not seen weighs exactly nothing
-                    x = see[w] >> k & 1u ? x : 0.f;
-                    y = see[w] >> (k + 1) & 1u ? y : 0.f;
-                }
             } else {
                 x = ex2_approx(x);
                 y = ex2_approx(y);
@@ -333,7 +317,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     unsigned char* ks = base + 2 * TB;
     unsigned char* vs = ks + KS * TB;
     auto& ctl = *reinterpret_cast<typename S::Ctrl*>(vs + VS * TB);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // uniform
 
     if (warp == 8 && lane == 0) {
         for (int i = 0; i < KS; ++i) {
@@ -387,7 +371,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
-    const uint32_t tmem = ctl.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
     PieceIter it{ctl.b0, ctl.rem0, ctl.left};
     Piece p{};
 
@@ -415,7 +399,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
         auto load = [&](const CUtensorMap* map, unsigned char* ring, uint64_t* full, uint64_t* empty, uint32_t stages,
                         uint32_t& n, const Ids& ids) {
             const uint32_t s = n % stages;
-            ok = ok && (n < stages || mbar_wait_bounded(empty + s, (n / stages - 1) & 1, kAttendTimeoutNs));
+            ok = ok && (n < stages || mbar_wait_short(empty + s, (n / stages - 1) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             unsigned char* dst = ring + s * TB;
@@ -456,9 +440,9 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
         // a wait ran out: nothing may be in flight when the CTA ends
         if (!ok) {
             for (uint32_t i = kn > KS ? kn - KS : 0; i < kn; ++i)
-                mbar_wait_bounded(&ctl.kfull[i % KS], (i / KS) & 1, kAttendTimeoutNs);
+                mbar_wait_short(&ctl.kfull[i % KS], (i / KS) & 1);
             for (uint32_t i = vn > VS ? vn - VS : 0; i < vn; ++i)
-                mbar_wait_bounded(&ctl.vfull[i % VS], (i / VS) & 1, kAttendTimeoutNs);
+                mbar_wait_short(&ctl.vfull[i % VS], (i / VS) & 1);
         }
     } else if (warp == 9) {
         // ---- matrix products
@@ -467,7 +451,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             bool ok = true;
             const uint32_t qaddr = smem_u32(qs), kaddr = smem_u32(ks), vaddr = smem_u32(vs);
             auto wait = [&](uint64_t* bar, uint32_t n) {
-                ok = ok && mbar_wait_bounded(bar, n & 1, kAttendTimeoutNs);
+                ok = ok && mbar_wait_short(bar, n & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 tcgen05_fence_after();
             };
@@ -596,7 +580,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                 if (tail) grid_dependency_wait();
                 // (after a wait that ran out every barrier is still met, so that no thread waits for good)
                 const int parity = sn & 1;
-                ok = ok && mbar_wait_bounded(&ctl.sfull[t], parity, kAttendTimeoutNs);
+                ok = ok && mbar_wait_short(&ctl.sfull[t], parity);
                 ++sn;
                 // V rows that nobody may see become zero before P V reads them: rows past the
                 // request and rows of the tree that are not finite (they make NaN of the nodes
@@ -610,7 +594,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     if (lane == 0) ctl.odd[t][parity][warp & 3] = bits;
                     if (t == 0 || p.split) {
                         const uint32_t n = vn + i;
-                        ok = ok && mbar_wait_bounded(&ctl.vfull[n % VS], (n / VS) & 1, kAttendTimeoutNs);
+                        ok = ok && mbar_wait_short(&ctl.vfull[n % VS], (n / VS) & 1);
                         if (past || bad) {
                             unsigned char* vrow = vs + (n % VS) * TB + r * 128;
 #pragma unroll
@@ -624,14 +608,21 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                 ok = __all_sync(0xffffffffu, ok);
                 tcgen05_fence_after();
                 if (live && ok) {
-                    // which columns this row sees, 32 to a word
-                    uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                     if (tail) {
-#pragma unroll
+                        // scores of what the row does not see become -inf, 32 columns at a time
+#pragma unroll 1
                         for (int w = 0; w < 4; ++w) {
-                            see[w] = mask_word(mask, pos0 + 32 * w - p.len);
-                            odd |= (see[w] & ctl.odd[t][parity][w]) != 0;
+                            const uint32_t see = mask_word(mask, pos0 + 32 * w - p.len);
+                            odd |= (see & ctl.odd[t][parity][w]) != 0;
+                            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+                            uint32_t x[32];
+                            tmem_load(x, lanes + s_at(t) + 32 * w);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(see >> k & 1u)) x[k] = 0xff800000u;
+                            tmem_store(lanes + s_at(t) + 32 * w, x);
                         }
+                        tmem_wait_st();
                     }
                     // Weights against the reference so far; only where some row of the warp rises
                     // too far over it for its weights to be held (and in the first tile of a
@@ -640,15 +631,13 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     float part = 0.f;
                     bool fresh = __any_sync(0xffffffffu, m == -INFINITY);  // a row without a reference
                     for (;;) {
-                        const float ref = m == -INFINITY ? 0.f : m;  // a row that sees nothing yet: all weights 0
                         if (!fresh) {
-                            part = tail ? tile_weights<T, true>(lanes + s_at(t), see, c, ref, packed)
-                                        : tile_weights<T, false>(lanes + s_at(t), see, c, ref, packed);
+                            // (a row that sees nothing yet: all weights 0)
+                            part = tile_weights<T>(lanes + s_at(t), c, m == -INFINITY ? 0.f : m, packed);
                             // (a sum that is NaN is not mended by another reference)
                             if (!__any_sync(0xffffffffu, part > kMostSum)) break;
                         }
-                        const float best = tail ? tile_top<true>(lanes + s_at(t), see) : tile_top<false>(lanes + s_at(t), see);
-                        const float top = best * c - H::kShift;
+                        const float top = tile_top(lanes + s_at(t)) * c - H::kShift;
                         if (!fresh && !__any_sync(0xffffffffu, top > m)) break;
                         const float f = top > m ? ex2_approx(m - top) : 1.f;  // 0 where there was nothing yet
                         if (top > m) m = top;
@@ -666,14 +655,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                         fresh = false;
                     }
                     l += part;
-                    // the weights go over the scores
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t s[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) s[k] = packed[16 * w + k];
-                        tmem_store(lanes + s_at(t) + 16 * w, s);
-                    }
+                    tmem_store(lanes + s_at(t), packed);         // over the scores
                     tmem_wait_st();
                 }
                 tcgen05_fence_before();
@@ -683,7 +665,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             vn += p.n;
             if (odd || !ok) l = NAN;
             const bool any = from < p.n;
-            if (any) ok = ok && mbar_wait_bounded(&ctl.ofull[t], on++ & 1, kAttendTimeoutNs);
+            if (any) ok = ok && mbar_wait_short(&ctl.ofull[t], on++ & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) l = NAN;
             tcgen05_fence_after();
