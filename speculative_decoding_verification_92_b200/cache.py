@@ -12,6 +12,8 @@ synchronises, so a whole step can be captured into a CUDA graph.
     ...                                                                    # tree_attention, tree_verify
     lens = cache_commit(k_cache, v_cache, page_table, lens, path)          # keep the accepted rows
     cache_resize(page_table, lens, refcount, page_size)                    # give the rest back
+
+``tree.TreeStep`` is this sequence.
 """
 from __future__ import annotations
 
@@ -129,6 +131,14 @@ def _call(fn, index, stream, *args):
         raise SpecVerifyError(status, fn.__name__)
 
 
+def _fresh(shape, dtype, device, stream):
+    """A new tensor that may be used on `stream` (None: the current one)."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)   # not given to others before the work there is done
+    return t
+
+
 def _table(page_table):
     if page_table.dim() != 2 or page_table.shape[1] < 1:
         raise ValueError("page_table must be [slots, max_pages]")
@@ -145,7 +155,7 @@ def cache_resize(page_table, lens, refcount, page_size, *, status=None, stream=N
     slots, max_pages = _table(page_table)
     dev = _cuda_index("page_table", page_table)
     if status is None:
-        status = torch.empty(slots, dtype=torch.int32, device=page_table.device)
+        status = _fresh(slots, torch.int32, page_table.device, stream)
     pages = refcount.shape
     if len(pages) != 1:
         raise ValueError("refcount must be [pages]")
@@ -167,7 +177,7 @@ def cache_commit(k_cache, v_cache, page_table, lens, path, *, out_lens=None, str
     dev = _cuda_index("page_table", page_table)
     c = _cache(k_cache, v_cache, dev)
     if out_lens is None:
-        out_lens = torch.empty(B, dtype=torch.int32, device=page_table.device)
+        out_lens = _fresh(B, torch.int32, page_table.device, stream)
     if path.dim() != 2:
         raise ValueError("path must be [B, width]")
     width = path.shape[1]
@@ -192,7 +202,7 @@ def cache_fork(k_cache, v_cache, page_table, lens, refcount, src, dst, *, status
         raise ValueError("src must be [forks]")
     n = src.shape[0]
     if status is None:
-        status = torch.empty(n, dtype=torch.int32, device=page_table.device)
+        status = _fresh(n, torch.int32, page_table.device, stream)
     table, stride = _int_rows("page_table", page_table, (slots, max_pages), dev)
     pages = k_cache.shape[-4]
     _call(_library().sv_cache_fork, dev, stream, c, table, stride, slots, max_pages,

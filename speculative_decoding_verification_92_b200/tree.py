@@ -15,9 +15,10 @@ import struct
 import torch
 
 from . import BF16, F32, library
-from .cache import _bad_tensor, _cache, _call, _cuda_index, _dense, _int_rows, _table
+from .cache import (_bad_tensor, _cache, _call, _cuda_index, _dense, _fresh, _int_rows, _table, cache_commit,
+                    cache_resize)
 
-__all__ = ["tree_attention", "tree_attention_workspace_bytes", "tree_verify", "MAX_NODES"]
+__all__ = ["tree_attention", "tree_attention_workspace_bytes", "tree_verify", "TreeStep", "MAX_NODES"]
 
 MAX_NODES = 256     # SV_MAX_NODES of the C header
 
@@ -98,13 +99,13 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     token per request is N = 1.  Calls that may run at the same time need
     separate workspaces."""
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _fresh(q.shape, q.dtype, q.device, stream)
     c, shape, ptrs, op = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
     B, N, dev = q.shape[0], q.shape[1], q.get_device()
     lib = _library()
     if workspace is None:
         n = lib.sv_tree_attention_workspace_bytes(shape, c)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        workspace = _fresh(max(n, 256), torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
     _call(lib.sv_tree_attention, dev, stream, shape, c, *ptrs, _dense("lens", lens, torch.int32, (B,), dev),
@@ -139,8 +140,7 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
     i32, nodes = torch.int32, (B, N)
     if out is None:
         at = target.device
-        out = (torch.empty(B, dtype=i32, device=at), torch.empty(nodes, dtype=i32, device=at),
-               torch.empty(nodes, dtype=i32, device=at))
+        out = _fresh(B, i32, at, stream), _fresh(nodes, i32, at, stream), _fresh(nodes, i32, at, stream)
         outs = [x.data_ptr() for x in out]
     else:
         outs = (_dense("out accept_len", out[0], i32, (B,), dev), _dense("out tokens", out[1], i32, nodes, dev),
@@ -152,3 +152,85 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
           _dense("counts", counts, i32, (B,), dev), _dense("uniforms", uniforms, torch.float32, nodes, dev),
           float(temperature), int(bool(greedy)), *outs)
     return out
+
+
+class TreeStep:
+    """A decoding step over a paged cache (``cache``), for trees of up to
+    ``nodes`` nodes per slot and a model with ``q_heads`` query heads:
+
+        step = TreeStep(k_cache, v_cache, page_table, lens, refcount, nodes, q_heads)
+        step.begin(parents, counts)                        # room for the trees
+        for layer in range(layers):                        # the target model
+            out = step.attention(layer, q, k, v)
+        accept_len, tokens, path = step.finish(target, draft, drafts, uniforms)
+
+    ``page_table``, ``lens`` and ``refcount`` are updated in place: ``begin``
+    takes pages for ``lens + counts`` rows, ``finish`` verifies, moves the
+    accepted rows behind the prefix, advances ``lens`` and gives surplus pages
+    back.  A slot that the free pages do not reach sits the step out as an
+    idle one (``status`` of the slot -1, nothing accepted, ``lens`` kept); so
+    does one whose length and count do not fit its row of the table.  Pages
+    that a slot holds past its rows are given back by either call.
+
+    The step owns its workspace and outputs (the next step overwrites them),
+    allocates nothing after it is built and never synchronises; everything
+    runs on the current stream, so one step can be captured into a CUDA graph
+    as ``graph.VerifyGraph`` captures a verification.  Two steps that may run at the
+    same time need a TreeStep each."""
+
+    def __init__(self, k_cache, v_cache, page_table, lens, refcount, nodes, q_heads):
+        if k_cache.dim() != 5:
+            raise ValueError("k_cache must be [layers, pages, page_size, heads, head_dim]")
+        if not 1 <= nodes <= MAX_NODES:
+            raise ValueError(f"nodes must be in [1, {MAX_NODES}], got {nodes}")
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.page_table, self.lens, self.refcount, self.nodes = page_table, lens, refcount, nodes
+        slots, dev = _table(page_table)[0], k_cache.device
+        heads, head_dim = k_cache.shape[3:]
+        _dense("lens", lens, torch.int32, (slots,), _cuda_index("k_cache", k_cache))
+        ints = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+        self.status, self.counts, self.parents = ints(slots), None, None
+        self._want, self._new_lens, self._full = ints(slots), ints(slots), torch.full_like(lens, nodes)
+        self._counts, self._trimmed = ints(slots), ints(slots)
+        self._verified = ints(slots), ints(slots, nodes), ints(slots, nodes)
+        q, k = (torch.empty(slots, nodes, h, head_dim, dtype=k_cache.dtype, device=dev) for h in (q_heads, heads))
+        n = tree_attention_workspace_bytes(q, k, k, k_cache[0], v_cache[0], page_table)
+        if n == 0 and slots > 0:
+            raise ValueError("no tree attention for a cache of this type, page size or head count")
+        self._workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+
+    def begin(self, parents=None, counts=None):
+        """Takes the pages of this step's trees (``parents [slots, nodes]``,
+        ``counts [slots]`` as in ``tree_attention``); returns ``status``."""
+        counts = self._full if counts is None else counts
+        if counts.dtype != torch.int32:
+            raise TypeError(f"counts must be {torch.int32}, got {counts.dtype}")
+        torch.clamp(counts, min=0, out=self._want)   # (a count or length that is not valid takes nothing away)
+        self._want += self.lens
+        torch.where(self.lens < 0, self.lens, self._want, out=self._want)
+        cache_resize(self.page_table, self._want, self.refcount, self.k_cache.shape[2], status=self.status)
+        # a slot without its pages is idle
+        torch.mul(counts, self.status + 1, out=self._counts)
+        self.parents, self.counts = parents, self._counts
+        return self.status
+
+    def attention(self, layer, q, k, v, *, scale=None, out=None):
+        """``tree_attention`` of one layer of the cache."""
+        return tree_attention(q, k, v, self.k_cache[layer], self.v_cache[layer], self.page_table, self.lens,
+                              self.parents, self._begun(), scale=scale, out=out, workspace=self._workspace)
+
+    def finish(self, target, draft, tokens, uniforms, temperature=1.0, greedy=False, *, V=None):
+        """``tree_verify`` of the step's trees; the cache then holds the
+        accepted path.  Returns ``(accept_len, tokens, path)``."""
+        out = tree_verify(target, draft, tokens, self.parents, self._begun(), uniforms, temperature, greedy, V=V,
+                          out=self._verified)
+        cache_commit(self.k_cache, self.v_cache, self.page_table, self.lens, out[2], out_lens=self._new_lens)
+        torch.where(self._new_lens < 0, self.lens, self._new_lens, out=self.lens)
+        cache_resize(self.page_table, self.lens, self.refcount, self.k_cache.shape[2], status=self._trimmed)
+        self.counts = None
+        return out
+
+    def _begun(self):
+        if self.counts is None:
+            raise RuntimeError("begin() comes first")
+        return self.counts
