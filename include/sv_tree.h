@@ -162,7 +162,7 @@ SV_API sv_status sv_cache_commit(const sv_cache *cache, const int32_t *page_tabl
  * id, slots in order.  out_status[slot] = 0, or -1 (the slot unchanged) when
  * lens[slot] < 0, max_pages is too small, an entry is not in [-1, pages) or
  * pages follow a -1; or when the free pages do not suffice for the slot and
- * all before it that miss some. */
+ * all before it that miss some.  out_status must not overlap lens. */
 SV_API sv_status sv_cache_resize(int32_t *page_table, int64_t table_stride, int32_t slots, int32_t max_pages,
                                  const int32_t *lens, int32_t page_size, int32_t *refcount, int32_t pages,
                                  int32_t *out_status, void *stream);
@@ -176,7 +176,8 @@ SV_API sv_status sv_cache_resize(int32_t *page_table, int64_t table_stride, int3
  * pages are not valid as above, or dst's entries are not (all unchanged); or
  * -2 when no free page is left for the ragged page (dst is left empty, its
  * length 0).  Rows of shared pages must not be written: a forked slot is
- * extended, not rewound below the length it was forked at. */
+ * extended, not rewound below the length it was forked at.  lens, src (or
+ * dst) and out_status must not overlap. */
 SV_API sv_status sv_cache_fork(const sv_cache *cache, int32_t *page_table, int64_t table_stride, int32_t slots,
                                int32_t max_pages, int32_t *lens, int32_t *refcount, const int32_t *src,
                                const int32_t *dst, int32_t forks, int32_t *out_status, void *stream);

@@ -367,6 +367,8 @@ commit_kernel(CopyParams c, const int32_t* table, int64_t stride, int max_pages,
     }
 }
 
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) { return a < b + m && b < a + n; }
+
 bool cache_ok(const sv_cache* c, CopyParams* out, sv_status* why) {
     *why = SV_EINVAL;
     if (!c || !c->k || !c->v || c->layers < 1 || c->pages < 1 || c->page_size < 1 || c->heads < 1 ||
@@ -411,9 +413,9 @@ extern "C" sv_status sv_cache_resize(int32_t* page_table, int64_t table_stride, 
     using namespace sv;
     if (table_stride == 0) table_stride = max_pages;
     if (slots < 0 || max_pages < 1 || page_size < 1 || pages < 1 || table_stride < max_pages) return SV_EINVAL;
-    if (!page_table || !lens || !refcount || !out_status) return SV_EINVAL;
-    if (slots > SV_MAX_SLOTS || int64_t(slots) * max_pages > 0x7fffffff) return SV_EUNSUPPORTED;
     if (slots == 0) return SV_OK;
+    if (!page_table || !lens || !refcount || !out_status || overlap(lens, slots, out_status, slots)) return SV_EINVAL;
+    if (slots > SV_MAX_SLOTS || int64_t(slots) * max_pages > 0x7fffffff) return SV_EUNSUPPORTED;
     const cudaError_t e = launch_pool(resize_kernel, int64_t(slots) * max_pages, pages, static_cast<cudaStream_t>(stream),
                                       page_table, table_stride, slots, max_pages, lens, page_size, refcount, pages,
                                       out_status);
@@ -429,9 +431,12 @@ extern "C" sv_status sv_cache_fork(const sv_cache* cache, int32_t* page_table, i
     if (!cache_ok(cache, &c, &why)) return why;
     if (table_stride == 0) table_stride = max_pages;
     if (slots < 1 || max_pages < 1 || forks < 0 || table_stride < max_pages) return SV_EINVAL;
-    if (!page_table || !lens || !refcount || !src || !dst || !out_status) return SV_EINVAL;
-    if (slots > SV_MAX_SLOTS || forks > SV_MAX_SLOTS) return SV_EUNSUPPORTED;
     if (forks == 0) return SV_OK;
+    if (!page_table || !lens || !refcount || !src || !dst || !out_status) return SV_EINVAL;
+    if (overlap(src, forks, out_status, forks) || overlap(dst, forks, out_status, forks) ||
+        overlap(lens, slots, out_status, forks) || overlap(lens, slots, src, forks) || overlap(lens, slots, dst, forks))
+        return SV_EINVAL;  // read again after they are written
+    if (slots > SV_MAX_SLOTS || forks > SV_MAX_SLOTS) return SV_EUNSUPPORTED;
     auto st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_pool(fork_kernel, 2 * int64_t(forks) * max_pages, c.pages, st, page_table, table_stride,
                                 slots, max_pages, lens, c.page_size, refcount, c.pages, src, dst, forks, out_status);
@@ -453,10 +458,10 @@ extern "C" sv_status sv_cache_commit(const sv_cache* cache, const int32_t* page_
     if (table_stride == 0) table_stride = max_pages;
     if (path_stride == 0) path_stride = width;
     if (B < 0 || max_pages < 1 || width < 1 || table_stride < max_pages || path_stride < width) return SV_EINVAL;
+    if (B == 0) return SV_OK;  // (an empty tensor's pointer may be null)
     if (!page_table || !lens || !path || !out_lens) return SV_EINVAL;
-    if (lens < out_lens + B && out_lens < lens + B) return SV_EINVAL;  // read by one CTA, written by another
+    if (overlap(lens, B, out_lens, B)) return SV_EINVAL;  // read by one CTA, written by another
     if (width > SV_MAX_NODES) return SV_EUNSUPPORTED;
-    if (B == 0) return SV_OK;
     const int64_t columns = 2 * int64_t(c.layers) * c.heads * c.head_words;
     const int64_t y = (columns + kCopyThreads - 1) / kCopyThreads;
     if (y > 65535) return SV_EUNSUPPORTED;

@@ -211,12 +211,12 @@ extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const s
                                        void* workspace, size_t workspace_bytes, void* stream) {
     using namespace sv;
     if (const sv_status why = attention_ok(s, cache); why != SV_OK) return why;
+    if (s->B == 0) return SV_OK;  // (an empty tensor's pointer may be null)
     if (!q || !k || !v || !page_table || !lens || !out || !workspace || !cache->k || !cache->v) return SV_EINVAL;
     if (!std::isfinite(scale) || workspace_bytes < workspace_layout(*s, *cache).total) return SV_EINVAL;
     for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(cache->k),
                           static_cast<const void*>(cache->v), static_cast<const void*>(workspace)})
         if (!tree_aligned16(p)) return SV_EINVAL;
-    if (s->B == 0) return SV_OK;
     const AttnWorkspace w = workspace_layout(*s, *cache);
     char* ws = static_cast<char*>(workspace);
     AttnParams a{static_cast<char*>(cache->k), static_cast<char*>(cache->v), cache->page_stride * 2,

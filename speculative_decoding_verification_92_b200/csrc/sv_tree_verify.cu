@@ -718,11 +718,11 @@ extern "C" sv_status sv_tree_verify(const sv_tree_shape* s, const void* target, 
     if (s->N > SV_MAX_NODES || s->V > SV_MAX_V) return SV_EUNSUPPORTED;
     const int64_t stride = s->row_stride ? s->row_stride : s->V;
     if (stride < s->V) return SV_EINVAL;
+    if (s->B == 0) return SV_OK;  // (an empty tensor's pointer may be null)
     if (!target || !tokens || !out_accept_len || !out_tokens || !out_path) return SV_EINVAL;
     if (!greedy && (!uniforms || !(temperature > 0.0) || !std::isfinite(temperature) ||
                     !std::isnormal(static_cast<float>(1.4426950408889634 / temperature))))
         return SV_EINVAL;
-    if (s->B == 0) return SV_OK;
     if (int64_t(s->B) * kTvMaxCluster > 0x7fffffff) return SV_EUNSUPPORTED;
     const int es = s->dtype == SV_BF16 ? 2 : 4;
     const bool vec = tree_aligned16(target) && (greedy || tree_aligned16(draft)) && stride * es % 16 == 0;

@@ -208,3 +208,26 @@ def test_refusals():
         (ValueError, lambda: cache.cache_fork(k, v, t, n, r, p[0], p[1, :1]))]:
         with pytest.raises(want):
             call()
+
+
+def test_nothing_to_do():
+    rng = np.random.default_rng(9)
+    e = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")
+    k, v = caches(rng, 2, 4, 16, 2, 8)
+    ref = t32([1, 0, 2, 0])
+    assert cache.cache_resize(e(0, 4), e(0), ref, 16).shape == (0,)
+    assert cache.cache_commit(k, v, e(0, 4), e(0), e(0, 3)).shape == (0,)
+    table = t32([[0, -1], [2, -1]])
+    assert cache.cache_fork(k, v, table, t32([5, 6]), ref, e(0), e(0)).shape == (0,)
+    assert ref.tolist() == [1, 0, 2, 0] and table.tolist() == [[0, -1], [2, -1]]
+
+
+def test_overlapping_tensors_are_refused():
+    lens = t32([5, 6])
+    with pytest.raises(SpecVerifyError):
+        cache.cache_resize(t32([[0, -1], [2, -1]]), lens, t32([1, 0, 1]), 16, status=lens)
+    both = t32([1, 1, 1])
+    k, v = caches(np.random.default_rng(10), 1, 3, 16, 2, 8)
+    with pytest.raises(SpecVerifyError):
+        cache.cache_fork(k, v, t32([[0, -1], [2, -1]]), t32([5, 6]), t32([1, 0, 1]), both[:1], both[1:2],
+                         status=both[1:2])

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from speculative_decoding_verification_92_b200 import Status, SpecVerifyError, tree
-from tree_reference import attention, attention_tolerance, make_parents
+from tree_reference import ancestors, attention, attention_tolerance, make_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -263,3 +263,50 @@ def _refused(want, c, **kw):
         args["out"] = None
     with pytest.raises(want):
         tree.tree_attention(**args)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "q"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_node_that_is_not_finite_harms_only_those_that_see_it(what, bad):
+    """Node 2's descendants and itself (for q: itself) are unspecified; every other node is what it is without it."""
+    for lens, N, g in (([120, 30], 20, 4), ([128, 1], 90, 3)):
+        c = Case(lens, [N, N], N, g=g, seed=16)
+        ref, tol = c.reference()
+        getattr(c, what)[:, 2] = bad
+        out = c.run()
+        torch.cuda.synchronize()
+        for b in range(2):
+            for i in range(N):
+                if i == 2 or (what != "q" and 2 in ancestors(c.parents[b], i)):
+                    continue
+                assert bool(((out[b, i].double() - ref[b, i]).abs() <= tol[b, i]).all()), (b, i)
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -2.0])
+def test_scales_of_either_sign_in_wide_trees(scale):
+    c = Case([130, 256, 0], [64, 40, 64], 64, g=4, width=3, seed=17)
+    c.scale = scale
+    c.check(c.run(scale=scale))
+
+
+def test_no_requests():
+    c = Case([5], [2], 2, seed=18)
+    none = lambda x: x[:0].contiguous()
+    out = tree.tree_attention(none(c.q), none(c.k), none(c.v), c.kc, c.vc, none(c.table), none(c.lens_t))
+    assert out.shape == (0,) + c.q.shape[1:]
+
+
+def test_a_call_s_own_tensors_on_another_stream():
+    """Output and workspace made by the call, used on `stream`, are not given
+    to later work of the current stream while the call may still run."""
+    c = Case([4000, 3000], [9, 9], 9, page=64, seed=19)
+    ref = c.reference()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(8):
+        outs.append(c.run(stream=side, out=None))
+        torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda")   # would land in the workspace's place
+    side.synchronize()
+    for out in outs:
+        c.check(out, ref)

@@ -1,5 +1,7 @@
 """tree_verify against the rule written out in 64 bits: whole numbers, so
 every answer has to be equal."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -254,3 +256,34 @@ def test_refusals():
         (sv.SpecVerifyError, (z, None, tok, par, cnt, u, float("nan")))]:
         with pytest.raises(want):
             tree.tree_verify(*args)
+
+
+@pytest.mark.parametrize("greedy", [False, True])
+@pytest.mark.parametrize("fill", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("draft", [False, True])
+def test_rows_that_are_not_finite_stay_in_bounds(fill, draft, greedy):
+    """Unspecified results, but a length, tokens and nodes that exist."""
+    B, N, V = 6, 7, 1000
+    gen = torch.Generator("cuda").manual_seed(9)
+    z = torch.randn(B, N, V, generator=gen, device="cuda")
+    y = torch.randn(B, N, V, generator=gen, device="cuda") if draft else None
+    z[0] = fill
+    z[1, :, ::3] = fill
+    z[2, :, 5] = fill
+    if draft:
+        y[3] = fill
+        y[4, :, 7] = fill
+        y[0] = fill
+    tokens = torch.randint(0, V, (B, N), generator=gen, device="cuda", dtype=torch.int32)
+    u = torch.rand(B, N, generator=gen, device="cuda")
+    n, tok, path = (x.cpu() for x in tree.tree_verify(z, y, tokens, None, None, u, 1.0, greedy))
+    for b in range(B):
+        j = int(n[b])
+        assert 0 <= j < N and bool(((tok[b, :j + 1] >= 0) & (tok[b, :j + 1] < V)).all())
+        assert bool((tok[b, j + 1:] == -1).all()) and path[b, :j + 1].tolist() == list(range(j + 1))
+
+
+def test_no_requests():
+    e = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device="cuda")
+    n, tok, path = tree.tree_verify(e(0, 3, 9, dt=torch.float32), None, e(0, 3), None, None, e(0, 3, dt=torch.float32))
+    assert n.shape == (0,) and tok.shape == path.shape == (0, 3)

@@ -85,7 +85,7 @@ EINVAL, EUNSUPPORTED, OK = Status.EINVAL, Status.EUNSUPPORTED, Status.OK
     (EINVAL, dict(q=None)), (EINVAL, dict(k=None)), (EINVAL, dict(v=None)), (EINVAL, dict(table=None)),
     (EINVAL, dict(lens=None)), (EINVAL, dict(out=None)), (EINVAL, dict(ws=None)), (EINVAL, dict(ws_bytes=64)),
     (EINVAL, dict(scale=math.nan)), (EINVAL, dict(scale=math.inf)), (EINVAL, dict(q=FAKE + 2)),
-    (EINVAL, dict(ws=FAKE + 8)), (OK, dict(s=dict(B=0)))])
+    (EINVAL, dict(ws=FAKE + 8)), (OK, dict(s=dict(B=0), q=None, k=None, v=None, table=None, lens=None, out=None))])
 def test_attention_arguments(want, kw):
     kw = dict(kw)
     if "s" in kw:
@@ -116,19 +116,20 @@ def verify(B=2, N=3, V=100, dtype=sv.F32, stride=0, target=FAKE, tokens=FAKE, un
     (EINVAL, dict(T=0.0)), (EINVAL, dict(T=-1.0)), (EINVAL, dict(T=math.nan)), (EINVAL, dict(T=math.inf)),
     (EINVAL, dict(T=1e-45)), (EINVAL, dict(T=1e300)), (EINVAL, dict(out=(None, FAKE, FAKE))),
     (EINVAL, dict(out=(FAKE, None, FAKE))), (EINVAL, dict(out=(FAKE, FAKE, None))), (OK, dict(B=0)),
-    (OK, dict(B=0, uniforms=None, greedy=1, T=0.0))])
+    (OK, dict(B=0, target=None, tokens=None, out=(None, None, None))), (OK, dict(B=0, uniforms=None, greedy=1, T=0.0))])
 def test_verify_arguments(want, kw):
     assert verify(**kw) == want
 
 
-def resize(table=FAKE, stride=4, slots=2, max_pages=4, lens=FAKE, page=16, ref=FAKE, pages=8, status=FAKE):
+def resize(table=FAKE, stride=4, slots=2, max_pages=4, lens=FAKE, page=16, ref=FAKE, pages=8, status=2 * FAKE):
     return cache._library().sv_cache_resize(table, stride, slots, max_pages, lens, page, ref, pages, status, None)
 
 
 @pytest.mark.parametrize("want,kw", [
     (EINVAL, dict(table=None)), (EINVAL, dict(lens=None)), (EINVAL, dict(ref=None)), (EINVAL, dict(status=None)),
     (EINVAL, dict(slots=-1)), (EINVAL, dict(max_pages=0)), (EINVAL, dict(page=0)), (EINVAL, dict(pages=-1)),
-    (EINVAL, dict(stride=3)), (EUNSUPPORTED, dict(slots=8193)), (OK, dict(slots=0))])
+    (EINVAL, dict(stride=3)), (EUNSUPPORTED, dict(slots=8193)), (EINVAL, dict(status=FAKE + 4)),
+    (OK, dict(slots=0, table=None, lens=None, status=None))])
 def test_resize_arguments(want, kw):
     assert resize(**kw) == want
 
@@ -143,7 +144,7 @@ def commit(c=None, table=FAKE, stride=4, B=2, max_pages=4, lens=FAKE, path=FAKE,
     (EUNSUPPORTED, dict(c=dict(dtype=7))), (EINVAL, dict(table=None)), (EINVAL, dict(lens=None)),
     (EINVAL, dict(path=None)), (EINVAL, dict(out=None)), (EINVAL, dict(out=FAKE)), (EINVAL, dict(out=FAKE + 4)), (EINVAL, dict(B=-1)), (EINVAL, dict(max_pages=0)),
     (EINVAL, dict(stride=3)), (EINVAL, dict(path_stride=2)), (EINVAL, dict(width=-1)),
-    (EUNSUPPORTED, dict(width=257, path_stride=257)), (OK, dict(B=0))])
+    (EUNSUPPORTED, dict(width=257, path_stride=257)), (OK, dict(B=0, table=None, lens=None, path=None, out=None))])
 def test_commit_arguments(want, kw):
     kw = dict(kw)
     if "c" in kw:
@@ -151,7 +152,8 @@ def test_commit_arguments(want, kw):
     assert commit(**kw) == want
 
 
-def fork(c=None, table=FAKE, stride=4, slots=4, max_pages=4, lens=FAKE, ref=FAKE, src=FAKE, dst=FAKE, n=2, status=FAKE):
+def fork(c=None, table=FAKE, stride=4, slots=4, max_pages=4, lens=FAKE, ref=FAKE, src=2 * FAKE, dst=3 * FAKE, n=2,
+         status=4 * FAKE):
     return cache._library().sv_cache_fork(c or kv(), table, stride, slots, max_pages, lens, ref, src, dst, n, status,
                                           None)
 
@@ -160,7 +162,8 @@ def fork(c=None, table=FAKE, stride=4, slots=4, max_pages=4, lens=FAKE, ref=FAKE
     (EINVAL, dict(c=dict(v=0))), (EINVAL, dict(table=None)), (EINVAL, dict(lens=None)), (EINVAL, dict(ref=None)),
     (EINVAL, dict(src=None)), (EINVAL, dict(dst=None)), (EINVAL, dict(status=None)), (EINVAL, dict(slots=-1)),
     (EINVAL, dict(n=-1)), (EINVAL, dict(stride=3)), (EUNSUPPORTED, dict(slots=8193)), (EUNSUPPORTED, dict(n=8193)),
-    (OK, dict(n=0))])
+    (EINVAL, dict(status=FAKE + 12)), (EINVAL, dict(status=2 * FAKE + 4)), (EINVAL, dict(status=3 * FAKE - 4)),
+    (EINVAL, dict(src=FAKE + 8)), (EINVAL, dict(dst=FAKE)), (OK, dict(n=0, src=None, dst=None, status=None))])
 def test_fork_arguments(want, kw):
     kw = dict(kw)
     if "c" in kw:
