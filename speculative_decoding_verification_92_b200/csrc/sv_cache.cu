@@ -393,15 +393,17 @@ bool cache_ok(const sv_cache* c, CopyParams* out, sv_status* why) {
     return true;
 }
 
-template <typename Kernel, typename... Args>
-cudaError_t launch_pool(Kernel k, int64_t entries, int pages, cudaStream_t st, const Args&... args) {
+template <auto kKernel, typename... Args>
+cudaError_t launch_pool(int64_t entries, int pages, cudaStream_t st, const Args&... args) {
     // one CTA while its 1024 threads see each entry a few times; the cluster's
     // barriers cost about a microsecond
     const int cluster = entries + pages > 16 * kPoolThreads ? kPoolMaxCluster : 1;
     const size_t smem = sizeof(PoolShared);
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    TreeDevice dev;
+    cudaError_t e = tree_device(&dev);
+    if (e == cudaSuccess) e = set_once<kKernel>(dev, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_dependent(k, dim3(static_cast<unsigned>(cluster)), kPoolThreads, smem, cluster, st, args...);
+    return launch_dependent(kKernel, dim3(static_cast<unsigned>(cluster)), kPoolThreads, smem, cluster, st, args...);
 }
 
 }  // namespace
@@ -416,7 +418,7 @@ extern "C" sv_status sv_cache_resize(int32_t* page_table, int64_t table_stride, 
     if (slots == 0) return SV_OK;
     if (!page_table || !lens || !refcount || !out_status || overlap(lens, slots, out_status, slots)) return SV_EINVAL;
     if (slots > SV_MAX_SLOTS || int64_t(slots) * max_pages > 0x7fffffff) return SV_EUNSUPPORTED;
-    const cudaError_t e = launch_pool(resize_kernel, int64_t(slots) * max_pages, pages, static_cast<cudaStream_t>(stream),
+    const cudaError_t e = launch_pool<&resize_kernel>(int64_t(slots) * max_pages, pages, static_cast<cudaStream_t>(stream),
                                       page_table, table_stride, slots, max_pages, lens, page_size, refcount, pages,
                                       out_status);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
@@ -438,7 +440,7 @@ extern "C" sv_status sv_cache_fork(const sv_cache* cache, int32_t* page_table, i
         return SV_EINVAL;  // read again after they are written
     if (slots > SV_MAX_SLOTS || forks > SV_MAX_SLOTS) return SV_EUNSUPPORTED;
     auto st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_pool(fork_kernel, 2 * int64_t(forks) * max_pages, c.pages, st, page_table, table_stride,
+    cudaError_t e = launch_pool<&fork_kernel>(2 * int64_t(forks) * max_pages, c.pages, st, page_table, table_stride,
                                 slots, max_pages, lens, c.page_size, refcount, c.pages, src, dst, forks, out_status);
     if (e != cudaSuccess) return SV_ECUDA;
     const int solid = c.head == int64_t(c.head_words) * 16 && c.row == c.heads * c.head;

@@ -222,10 +222,14 @@ struct PieceIter {
 
 // ---------------------------------------------------------------------------
 
+// All of it stays below 196 KiB (164 KiB for D = 64), the step of the carve-out
+// that leaves 60 KiB (92 KiB) of L1 for the page table, the masks, Q and the
+// softmax warps' few spilled registers.  A third stage of K leaves 28 KiB and
+// costs 7 % of a batch of chains (107 us against 100) although more is in flight.
 template <int D>
 struct AttendSmem {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kKStages = D == 128 ? 3 : 5;
+    static constexpr int kKStages = D == 128 ? 2 : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
     struct Ctrl {
         uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
@@ -237,7 +241,8 @@ struct AttendSmem {
         uint32_t tmem;
         int32_t b0, rem0;
     };
-    static constexpr size_t bytes() { return 1024 + size_t(2 + kKStages + kVStages) * kTileBytes + sizeof(Ctrl); }
+    static_assert(kTileBytes % 1024 == 0, "the 128-byte swizzle repeats every 1024 bytes");
+    static constexpr size_t bytes() { return size_t(2 + kKStages + kVStages) * kTileBytes + sizeof(Ctrl); }
 };
 
 // The 32 mask bits of cached rows a0 .. a0 + 31 of the tree (rows before the
@@ -311,10 +316,8 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
     // tensor memory: scores (then weights) of the two groups, then their results
     auto s_at = [](int t) { return static_cast<uint32_t>(t * kTile); };
     auto o_at = [](int t) { return static_cast<uint32_t>(2 * kTile + t * D); };
-    extern __shared__ unsigned char raw[];
-    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* qs = base;               // two tiles of Q
-    unsigned char* ks = base + 2 * TB;
+    extern __shared__ __align__(1024) unsigned char qs[];  // two tiles of Q, then K, V and the rest
+    unsigned char* ks = qs + 2 * TB;
     unsigned char* vs = ks + KS * TB;
     auto& ctl = *reinterpret_cast<typename S::Ctrl*>(vs + VS * TB);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // uniform

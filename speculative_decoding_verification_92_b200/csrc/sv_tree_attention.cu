@@ -187,8 +187,8 @@ cudaError_t run(const AttnParams& a, const sv_cache& c, cudaStream_t st) {
     const int splits = (a.N + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
     e = launch_dependent(tree_prepare_kernel<T>, dim3(a.B, splits), kPrepThreads, 0, 1, st, a);
     if (e != cudaSuccess) return e;
-    auto k = tree_attend_kernel<T, D>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(AttendSmem<D>::bytes()));
+    constexpr auto k = &tree_attend_kernel<T, D>;
+    e = set_once<k>(dev, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(AttendSmem<D>::bytes()));
     if (e != cudaSuccess) return e;
     const int ctas = dev.sm_count < kAttendMaxCtas ? dev.sm_count : kAttendMaxCtas;
     e = launch_dependent(k, dim3(ctas), kAttendThreads, AttendSmem<D>::bytes(), 1, st, a, kmap, vmap);

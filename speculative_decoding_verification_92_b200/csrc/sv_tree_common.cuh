@@ -3,6 +3,7 @@
 // the host-side facts of the current device.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -36,16 +37,36 @@ __device__ __forceinline__ void st_cluster_u64(void* p, uint32_t rank, uint64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Host side.
+// Host side.  (Internal linkage: what a copy of the library remembers about
+// its kernels does not hold for another copy in the same process.)
+namespace {
+
+constexpr int kKnownDevices = 64;  // facts of devices past these are asked for in every call
 
 struct TreeDevice {
-    int sm_count = 0;
+    int index = 0, sm_count = 0;
 };
 
 inline cudaError_t tree_device(TreeDevice* d) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->sm_count, cudaDevAttrMultiProcessorCount, dev);
+    static std::atomic<int> sms[kKnownDevices];
+    cudaError_t e = cudaGetDevice(&d->index);
+    if (e != cudaSuccess) return e;
+    const bool known = d->index < kKnownDevices;
+    d->sm_count = known ? sms[d->index].load(std::memory_order_relaxed) : 0;
+    if (d->sm_count > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(&d->sm_count, cudaDevAttrMultiProcessorCount, d->index);
+    if (e == cudaSuccess && known) sms[d->index].store(d->sm_count, std::memory_order_relaxed);
+    return e;
+}
+
+// Sets an attribute that kernel `kKernel` needs, once per device.
+template <auto kKernel>
+cudaError_t set_once(const TreeDevice& d, cudaFuncAttribute attribute, int value) {
+    static std::atomic<uint64_t> done;
+    const uint64_t bit = d.index < kKnownDevices ? uint64_t(1) << d.index : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, attribute, value);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 
@@ -70,6 +91,8 @@ cudaError_t launch_dependent(Kernel k, dim3 grid, int threads, size_t smem, int 
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
+
+}  // namespace
 
 inline bool tree_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

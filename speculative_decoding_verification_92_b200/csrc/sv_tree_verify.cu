@@ -694,9 +694,11 @@ cudaError_t launch(TreeVerifyParams prm, int B, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int C = cluster_for(B, prm.V, Logit<T>::kSize, dev.sm_count);
     const bool roomy = int64_t(B) * C <= 2 * int64_t(dev.sm_count);
-    auto k = roomy ? tree_verify_kernel<T, kVec, kGreedy, 2> : tree_verify_kernel<T, kVec, kGreedy, kTvCtasPerSm>;
+    constexpr auto few = &tree_verify_kernel<T, kVec, kGreedy, 2>, many = &tree_verify_kernel<T, kVec, kGreedy, kTvCtasPerSm>;
+    const auto k = roomy ? few : many;
     if (C > 8) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = roomy ? set_once<few>(dev, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
+                  : set_once<many>(dev, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     const int step = Batch<T, kVec, 1>::kStep;  // a warp's vector
