@@ -580,32 +580,27 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
             for (int i = from; i < p.n; i += step) {
                 const int pos0 = (p.first + i) * kTile;
                 const bool tail = reads_new_rows(p, p.first + i);  // holds rows of the tree, or past it
-                if (tail) grid_dependency_wait();
+                bool clear = false, bad = false;
+                uint32_t see0, see1, see2, see3;                   // which columns this row sees, 32 to a word
+                if (tail) {
+                    // (what is read here is on its way while the scores are waited for)
+                    grid_dependency_wait();
+                    const int a0 = pos0 + r - p.len;
+                    const bool past = pos0 + r >= p.rows;
+                    bad = !past && a0 >= 0 && a.odd[int64_t(p.b) * a.N + a0] != 0;
+                    clear = past || bad;
+                    see0 = mask_word(mask, pos0 - p.len);
+                    see1 = mask_word(mask, pos0 + 32 - p.len);
+                    see2 = mask_word(mask, pos0 + 64 - p.len);
+                    see3 = mask_word(mask, pos0 + 96 - p.len);
+                }
                 // (after a wait that ran out every barrier is still met, so that no thread waits for good)
                 const int parity = sn & 1;
                 ok = ok && mbar_wait_short(&ctl.sfull[t], parity);
                 ++sn;
-                // V rows that nobody may see become zero before P V reads them: rows past the
-                // request and rows of the tree that are not finite (they make NaN of the nodes
-                // that see them, below).  The scores of this tile say that the products two tiles back
-                // are done, so the V stage is in this tile's phase or the one before it.
                 if (tail) {
-                    const int a0 = pos0 + r - p.len;
-                    const bool past = pos0 + r >= p.rows;
-                    const bool bad = !past && a0 >= 0 && a.odd[int64_t(p.b) * a.N + a0] != 0;
                     const uint32_t bits = __ballot_sync(0xffffffffu, bad);
                     if (lane == 0) ctl.odd[t][parity][warp & 3] = bits;
-                    if (t == 0 || p.split) {
-                        const uint32_t n = vn + i;
-                        ok = ok && mbar_wait_short(&ctl.vfull[n % VS], (n / VS) & 1);
-                        if (past || bad) {
-                            unsigned char* vrow = vs + (n % VS) * TB + r * 128;
-#pragma unroll
-                            for (int x = 0; x < D / 8; ++x)
-                                *reinterpret_cast<uint4*>(vrow + (x / 8) * (kTile * 128) + (x % 8) * 16) = uint4{0, 0, 0, 0};
-                        }
-                        fence_async_shared();
-                    }
                     named_barrier_sync(1 + t, kTile);            // the group's bits are written
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -615,7 +610,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                         // scores of what the row does not see become -inf, 32 columns at a time
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w) {
-                            const uint32_t see = mask_word(mask, pos0 + 32 * w - p.len);
+                            const uint32_t see = w < 2 ? (w == 0 ? see0 : see1) : (w == 2 ? see2 : see3);
                             odd |= (see & ctl.odd[t][parity][w]) != 0;
                             if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
                             uint32_t x[32];
@@ -660,6 +655,21 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     l += part;
                     tmem_store(lanes + s_at(t), packed);         // over the scores
                     tmem_wait_st();
+                }
+                // V rows that nobody may see become zero before P V reads them: rows past the
+                // request and rows of the tree that are not finite (they make NaN of the nodes
+                // that see them, by `odd`).  The scores of this tile say that the products two tiles back
+                // are done, so the V stage is in this tile's phase or the one before it.
+                if (tail && (t == 0 || p.split)) {
+                    const uint32_t n = vn + i;
+                    ok = ok && mbar_wait_short(&ctl.vfull[n % VS], (n / VS) & 1);
+                    if (clear) {
+                        unsigned char* vrow = vs + (n % VS) * TB + r * 128;
+#pragma unroll 1
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(vrow + (x / 8) * (kTile * 128) + (x % 8) * 16) = uint4{0, 0, 0, 0};
+                    }
+                    fence_async_shared();
                 }
                 tcgen05_fence_before();
                 __syncwarp();
