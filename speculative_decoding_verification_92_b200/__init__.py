@@ -4,8 +4,9 @@ The work runs in ``libspecverify.so`` (CUDA kernels for sm_100a, declared in
 ``include/spec_verify.h``).  This module is a thin ctypes binding: it checks
 tensor shapes, dtypes and devices, passes raw pointers and the current CUDA
 stream, and turns status codes into exceptions.  ``host`` binds the host-side
-drafters and schedulers of ``include/sv_host.h``; ``graph`` replays a whole
-step as one CUDA graph.  PyTorch is used only for device memory
+drafters and schedulers of ``include/sv_host.h``; ``tree`` and ``cache`` bind
+``include/sv_tree.h``, decoding steps that draft a tree over a paged cache;
+``graph`` replays a whole step as one CUDA graph.  PyTorch is used only for device memory
 and streams.  There is no CPU fallback: without the built library every call
 raises.
 

@@ -6,6 +6,13 @@
 // does not depend on the order of any atomic: reference counts are sums, and
 // a page's place in the hand-out is its rank among the free pages.  The
 // copies are plain streams of 16-byte words, bound by memory.
+//
+// Measured on the device.  Page accounting of 64 slots 7 to 10 us, a chain of
+// dependent loads and barriers; compaction of 64 trees through 32 layers (23
+// MB) 12 us; 64 forks through 32 layers, 111 MB: 12 us of accounting and 22 us
+// of copies, 5 TB/s.  The host's part of a call from Python is about 9 us, so
+// that eager steps are bound by it and captured ones are not: resize, commit
+// and resize take 35 us eagerly, 23 us (64 trees) and 10 us (2 trees) replayed.
 #include <cstdint>
 
 #include <cuda_runtime.h>

@@ -27,6 +27,16 @@
 // CTAs of a cluster split the vocabulary; the more requests, the smaller the
 // cluster, so that all of them run at once (cluster_for).  A warp owns one
 // contiguous range of the row, which is the unit the final draw looks up.
+//
+// Measured on the device, V = 151936 in bf16.  A visit takes 3.7 us for one
+// request and 8.8 us for 64 (their rows alone 3 us at copy rate); greedy 2.1
+// and 5.9.  A leaf, which needs the 64-bit pass and the draw, 10 and 30 us, of
+// them the draw 3 and 7.  128 trees of 40 nodes: 92 us; 64 trees of 13 nodes
+// with draft logits in fp32 (V = 128256): 112 us.  Four CTAs per SM with 64
+// registers against two with 128: 92 to 113 us and 112 to 134, although the
+// leaf alone gains (30 to 26).  Batches loaded ahead of their use cost 10 us
+// (spills); rows of the first child brought to L2 while its parent is summed
+// gain 1 us when greedy and cost 4 to 10 us with sums.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
