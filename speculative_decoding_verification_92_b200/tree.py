@@ -172,11 +172,11 @@ class TreeStep:
     does one whose length and count do not fit its row of the table.  Pages
     that a slot holds past its rows are given back by either call.
 
-    The step owns its workspace and outputs (the next step overwrites them),
-    allocates nothing after it is built and never synchronises; everything
-    runs on the current stream, so one step can be captured into a CUDA graph
-    as ``graph.VerifyGraph`` captures a verification.  Two steps that may run at the
-    same time need a TreeStep each."""
+    The step owns its workspace and the outputs of ``finish`` (the next step
+    overwrites them) and never synchronises; everything runs on the current
+    stream, so one step can be captured into a CUDA graph as
+    ``graph.VerifyGraph`` captures a verification.  Two steps that may run at
+    the same time need a TreeStep each."""
 
     def __init__(self, k_cache, v_cache, page_table, lens, refcount, nodes, q_heads):
         if k_cache.dim() != 5:
