@@ -67,7 +67,7 @@ struct AttnParams {
     char* vc;
     int64_t page_stride, row_stride, head_stride;  // of the cache, in bytes
     int32_t pages, page_size, heads, head_dim;
-    int32_t B, N, q_heads, max_pages;
+    int32_t B, N, q_heads, group, max_pages;  // group: query heads per key head
     int64_t table_stride;
     int64_t qb, qn, qh, kb, kn, kh, vb, vn, vh, ob, on, oh;  // in bytes
     const char* q;
@@ -155,7 +155,7 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
 // The line of tiles.
 
 __device__ __forceinline__ int groups_of(const AttnParams& a, int count) {
-    return (count * (a.q_heads / a.heads) + kUnitRows - 1) / kUnitRows;
+    return (count * (a.group) + kUnitRows - 1) / kUnitRows;
 }
 // Cached rows of request b with its nodes, 0 where there is nothing to do
 // (what tree_prepare_kernel finds wrong beyond this is left to it).
@@ -211,7 +211,7 @@ struct PieceIter {
             ++b;
             rem = 0;
         }
-        const int g = a.q_heads / a.heads, R = (rows - len) * g;
+        const int g = a.group, R = (rows - len) * g;
         const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
         const int unit = rem / tiles;
         p.b = b;
@@ -556,7 +556,7 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
         // ---- softmax: group t, row r (a lane of tensor memory)
         const int t = warp >> 2, r = tid & (kTile - 1);
         const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21);
-        const int g = a.q_heads / a.heads;
+        const int g = a.group;
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
         const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
         uint32_t sn = 0, on = 0, vn = 0;
@@ -677,11 +677,15 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                 if (tail && (t == 0 || p.split)) {
                     const uint32_t n = vn + i;
                     ok = ok && mbar_wait_short(&ctl.vfull[n % VS], (n / VS) & 1);
-                    if (clear) {
-                        unsigned char* vrow = vs + (n % VS) * TB + r * 128;
+                    const uint32_t rows = __ballot_sync(0xffffffffu, clear);
+                    // (eight lanes to a row's 128 bytes: a thread per row would write to the same banks)
+                    unsigned char* at = vs + (n % VS) * TB + (warp & 3) * (32 * 128) + lane * 16;
 #pragma unroll 1
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(vrow + (x / 8) * (kTile * 128) + (x % 8) * 16) = uint4{0, 0, 0, 0};
+                    for (int x = 0; x < 8 && rows != 0; ++x) {
+                        if (!(rows >> (4 * x + lane / 8) & 1u)) continue;
+#pragma unroll
+                        for (int d = 0; d < D / 64; ++d)
+                            *reinterpret_cast<uint4*>(at + x * (4 * 128) + d * (kTile * 128)) = uint4{0, 0, 0, 0};
                     }
                     fence_async_shared();
                 }
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
         grid_dependency_wait();
         return;
     }
-    const int g = a.q_heads / a.heads, R = (rows - len) * g;
+    const int g = a.group, R = (rows - len) * g;
     const int groups = (R + kUnitRows - 1) / kUnitRows, tiles = (rows + kTile - 1) / kTile;
     const int row0 = (unit % groups) * kUnitRows, r = blockIdx.y * 32 + lane;
     if (unit >= a.heads * groups || row0 + static_cast<int>(blockIdx.y) * 32 >= R) {

@@ -193,7 +193,7 @@ cudaError_t run(const AttnParams& a, const sv_cache& c, cudaStream_t st) {
     const int ctas = dev.sm_count < kAttendMaxCtas ? dev.sm_count : kAttendMaxCtas;
     e = launch_dependent(k, dim3(ctas), kAttendThreads, AttendSmem<D>::bytes(), 1, st, a, kmap, vmap);
     if (e != cudaSuccess) return e;
-    const int g = a.q_heads / a.heads, units = a.heads * ((a.N * g + kUnitRows - 1) / kUnitRows);
+    const int units = a.heads * ((a.N * a.group + kUnitRows - 1) / kUnitRows);
     return launch_dependent(tree_join_kernel<T, D>, dim3(static_cast<unsigned>(a.B * units), a.slot_rows / 32),
                             kJoinThreads, 0, 1, st, a, units, ctas);
 }
@@ -221,7 +221,7 @@ extern "C" sv_status sv_tree_attention(const sv_tree_attention_shape* s, const s
     char* ws = static_cast<char*>(workspace);
     AttnParams a{static_cast<char*>(cache->k), static_cast<char*>(cache->v), cache->page_stride * 2,
                  cache->row_stride * 2, cache->head_stride * 2, cache->pages, cache->page_size, cache->heads,
-                 cache->head_dim, s->B, s->N, s->q_heads, s->max_pages,
+                 cache->head_dim, s->B, s->N, s->q_heads, s->q_heads / cache->heads, s->max_pages,
                  s->table_stride ? s->table_stride : s->max_pages,
                  s->q_stride_b * 2, s->q_stride_n * 2, s->q_stride_h * 2, s->k_stride_b * 2, s->k_stride_n * 2,
                  s->k_stride_h * 2, s->v_stride_b * 2, s->v_stride_n * 2, s->v_stride_h * 2, s->o_stride_b * 2,
