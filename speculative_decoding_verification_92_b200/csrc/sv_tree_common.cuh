@@ -59,14 +59,34 @@ inline cudaError_t tree_device(TreeDevice* d) {
     return e;
 }
 
-// Sets an attribute that kernel `kKernel` needs, once per device.
+// The current context's id, which no later context has again; 0 where the
+// driver cannot tell.
+inline unsigned long long tree_context() {
+    using GetCurrent = int (*)(void**);
+    using GetId = int (*)(void*, unsigned long long*);
+    auto entry = [](const char* name) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint(name, &f, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess ? f : nullptr;
+    };
+    static const GetCurrent get_current = reinterpret_cast<GetCurrent>(entry("cuCtxGetCurrent"));
+    static const GetId get_id = reinterpret_cast<GetId>(entry("cuCtxGetId"));
+    void* context = nullptr;
+    unsigned long long id = 0;
+    if (!get_current || !get_id || get_current(&context) != 0 || !context || get_id(context, &id) != 0) return 0;
+    return id;
+}
+
+// Sets an attribute that kernel `kKernel` needs, once per device and context
+// (attributes live in the context).
 template <auto kKernel>
 cudaError_t set_once(const TreeDevice& d, cudaFuncAttribute attribute, int value) {
-    static std::atomic<uint64_t> done;
-    const uint64_t bit = d.index < kKnownDevices ? uint64_t(1) << d.index : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    static std::atomic<unsigned long long> set_in[kKnownDevices];
+    const unsigned long long context = d.index < kKnownDevices ? tree_context() : 0;
+    if (context != 0 && set_in[d.index].load(std::memory_order_relaxed) == context) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kKernel, attribute, value);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    if (e == cudaSuccess && context != 0) set_in[d.index].store(context, std::memory_order_relaxed);
     return e;
 }
 
