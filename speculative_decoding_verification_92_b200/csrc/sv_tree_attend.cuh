@@ -777,12 +777,17 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
 }
 
 // Joins the parts of units that were cut: 32 rows of one unit per CTA, a lane
-// per row, the columns spread over the warps.
+// per row, kCols columns of four per warp, the rest over blockIdx.z.  Usually
+// there are two or three parts; few units over a long axis have many, and
+// their CTAs are few: then a warp takes one column and loads eight parts at a
+// time (sv_tree_attention.cu chooses).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-template <typename T, int D>
+template <typename T, int D, int kCols>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParams a, int units, int ctas) {
-    __shared__ int64_t sums[2][kJoinThreads / 32];
+    __shared__ int64_t sums[2][kJoinWarps];
+    __shared__ float tops[kJoinWarps][32];
     const int b = blockIdx.x / units, unit = blockIdx.x % units;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int len;
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
     }
     __syncthreads();
     before = all = 0;
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
         before += sums[0][w];
         all += sums[1][w];
     }
@@ -823,15 +828,24 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
     const int64_t u0 = before + int64_t(unit) * tiles;
     const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + tiles - 1) / per);
     grid_dependency_wait();
-    if (c0 == c1 || row0 + r >= R || r >= kUnitRows || a.ok[b] == 0) return;
+    if (c0 == c1 || a.ok[b] == 0) return;
+    const bool in = row0 + r < R && r < kUnitRows;
     float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * int64_t(c) + (c == c0)) * a.slot_rows + r].x);
+    if (in)
+#pragma unroll 4
+        for (int c = c0 + warp; c <= c1; c += kJoinWarps)
+            M = fmaxf(M, a.part_ml[(2 * int64_t(c) + (c == c0)) * a.slot_rows + r].x);
+    tops[warp][lane] = M;
+    __syncthreads();
+    if (!in) return;
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, tops[w][lane]);
     const float ref = M == -INFINITY ? 0.f : M;
     const int node = (row0 + r) / g, h = (unit / groups) * g + (row0 + r) % g;
     char* dst = a.out + b * a.ob + node * a.on + h * a.oh;
-    constexpr int kCols = D / 4 / (kJoinThreads / 32);  // float4 columns of a warp
+    const int col0 = (blockIdx.z * kJoinWarps + warp) * kCols;
     float4 o[kCols] = {};
     float l = 0.f;
+#pragma unroll kCols == 1 ? 8 : 2
     for (int c = c0; c <= c1; ++c) {
         const int64_t slot = 2 * int64_t(c) + (c == c0);
         const float2 ml = a.part_ml[slot * a.slot_rows + r];
@@ -839,7 +853,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
         l += ml.y * f;
 #pragma unroll
         for (int k = 0; k < kCols; ++k) {
-            const float4 v = a.part_o[(slot * (D / 4) + warp * kCols + k) * a.slot_rows + r];
+            const float4 v = a.part_o[(slot * (D / 4) + col0 + k) * a.slot_rows + r];
             o[k].x = fmaf(v.x, f, o[k].x);
             o[k].y = fmaf(v.y, f, o[k].y);
             o[k].z = fmaf(v.z, f, o[k].z);
@@ -849,7 +863,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnParam
     const float inv = 1.f / l;
 #pragma unroll
     for (int k = 0; k < kCols; ++k)
-        *reinterpret_cast<uint2*>(dst + (warp * kCols + k) * 8) =
+        *reinterpret_cast<uint2*>(dst + (col0 + k) * 8) =
             uint2{Half<T>::pack(o[k].x * inv, o[k].y * inv), Half<T>::pack(o[k].z * inv, o[k].w * inv)};
 }
 

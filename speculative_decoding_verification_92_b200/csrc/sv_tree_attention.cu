@@ -194,8 +194,16 @@ cudaError_t run(const AttnParams& a, const sv_cache& c, cudaStream_t st) {
     e = launch_dependent(k, dim3(ctas), kAttendThreads, AttendSmem<D>::bytes(), 1, st, a, kmap, vmap);
     if (e != cudaSuccess) return e;
     const int units = a.heads * ((a.N * a.group + kUnitRows - 1) / kUnitRows);
-    return launch_dependent(tree_join_kernel<T, D>, dim3(static_cast<unsigned>(a.B * units), a.slot_rows / 32),
-                            kJoinThreads, 0, 1, st, a, units, ctas);
+    dim3 grid(static_cast<unsigned>(a.B * units), a.slot_rows / 32);
+    constexpr int kCols = D / 4 / kJoinWarps;  // of a warp, where a CTA has all columns
+    // Few units: their many parts are spread over more CTAs (two requests with one key head over
+    // 12600 rows, 50 parts each: 72 us without, 27 with; many units, which have few parts: 93 us
+    // for a batch of chains without, 100 with, 191 and 197 for long trees).
+    if (int64_t(grid.x) * grid.y <= 2 * ctas) {
+        grid.z = kCols;
+        return launch_dependent(tree_join_kernel<T, D, 1>, grid, kJoinThreads, 0, 1, st, a, units, ctas);
+    }
+    return launch_dependent(tree_join_kernel<T, D, kCols>, grid, kJoinThreads, 0, 1, st, a, units, ctas);
 }
 
 }  // namespace

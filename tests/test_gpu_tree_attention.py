@@ -130,6 +130,12 @@ def test_one_long_request():
     Case([20011], [2], 2, Hkv=1, g=2, page=16, seed=5).check()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,g,lens", [(3, 7, [12600, 9000]), (64, 4, [18000]), (1, 1, [30000, 5, 0])])
+def test_few_units_cut_into_many_parts(N, g, lens, D):
+    Case(lens, [N] * len(lens), N, Hkv=1, g=g, D=D, page=16, seed=20).check()
+
+
 def test_many_short_requests():
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 200, 300).tolist()
