@@ -38,6 +38,7 @@ _SIGNATURES = {
 }
 _LOGIT_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 _LIB = None
+_WORKSPACE = {}    # bytes by sizes
 
 
 def _library():
@@ -61,20 +62,33 @@ def _rows(what, t, shape, dtype, index):
 
 
 def _attention_shapes(q, k, v, out, k_cache, v_cache, page_table):
-    if q.dim() != 4 or k_cache.dim() != 4:
+    qshape, cshape = q.shape, k_cache.shape
+    if len(qshape) != 4 or len(cshape) != 4:
         raise ValueError("q must be [B, N, q_heads, head_dim], the caches [pages, page_size, heads, head_dim]")
-    B, N, Hq, _ = q.shape
-    heads, D = k_cache.shape[2:]
+    B, N, Hq, D = qshape
+    heads = cshape[2]
     dt, dev = k_cache.dtype, _cuda_index("k_cache", k_cache)
     c = _cache(k_cache, v_cache, dev)
-    kv = (B, N, heads, D)
-    qp, *qs = _rows("q", q, (B, N, Hq, D), dt, dev)
+    full, kv = (B, N, Hq, cshape[3]), (B, N, heads, cshape[3])
+    qp, *qs = _rows("q", q, full, dt, dev)
     kp, *ks = _rows("k", k, kv, dt, dev)
     vp, *vs = _rows("v", v, kv, dt, dev)
-    op, *os = _rows("out", out, (B, N, Hq, D), dt, dev)
+    op, *os = _rows("out", out, full, dt, dev)
     max_pages = _table(page_table)[1]
     table, stride = _int_rows("page_table", page_table, (B, max_pages), dev)
-    return c, _ATTENTION_SHAPE.pack(B, N, Hq, max_pages, stride, *qs, *ks, *vs, *os), (qp, kp, vp, table), op
+    return (c, _ATTENTION_SHAPE.pack(B, N, Hq, max_pages, stride, *qs, *ks, *vs, *os), (qp, kp, vp, table), op,
+            (B, N, Hq, heads, D, dev))
+
+
+def _workspace_bytes(c, shape, sizes):
+    """Asked for once per sizes: it depends on nothing else, and asking takes
+    as long as a tensor's checks."""
+    n = _WORKSPACE.get(sizes)
+    if n is None:
+        n = int(_library().sv_tree_attention_workspace_bytes(shape, c))
+        if n and len(_WORKSPACE) < 4096:
+            _WORKSPACE[sizes] = n
+    return n
 
 
 def tree_attention_workspace_bytes(q, k, v, k_cache, v_cache, page_table) -> int:
@@ -100,17 +114,19 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     separate workspaces."""
     if out is None:
         out = _fresh(q.shape, q.dtype, q.device, stream)
-    c, shape, ptrs, op = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
-    B, N, dev = q.shape[0], q.shape[1], q.get_device()
-    lib = _library()
+    c, shape, ptrs, op, sizes = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
+    B, N, _, _, D, dev = sizes
     if workspace is None:
-        n = lib.sv_tree_attention_workspace_bytes(shape, c)
-        workspace = _fresh(max(n, 256), torch.uint8, q.device, stream)
+        n = max(_workspace_bytes(c, shape, sizes), 256)
+        workspace = _fresh(n, torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
-    _call(lib.sv_tree_attention, dev, stream, shape, c, *ptrs, _dense("lens", lens, torch.int32, (B,), dev),
-          _dense("parents", parents, torch.int32, (B, N), dev), _dense("counts", counts, torch.int32, (B,), dev),
-          k_cache.shape[3] ** -0.5 if scale is None else float(scale), op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    else:
+        n = workspace.numel() * workspace.element_size()
+    nodes = (B, N)
+    _call(_library().sv_tree_attention, dev, stream, shape, c, *ptrs, _dense("lens", lens, torch.int32, (B,), dev),
+          _dense("parents", parents, torch.int32, nodes, dev), _dense("counts", counts, torch.int32, (B,), dev),
+          D ** -0.5 if scale is None else float(scale), op, workspace.data_ptr(), n)
     return out
 
 
