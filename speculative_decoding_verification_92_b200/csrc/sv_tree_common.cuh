@@ -36,6 +36,8 @@ __device__ __forceinline__ void st_cluster_u64(void* p, uint32_t rank, uint64_t 
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---------------------------------------------------------------------------
 // Host side.  (Internal linkage: what a copy of the library remembers about
 // its kernels does not hold for another copy in the same process.)

@@ -35,8 +35,7 @@
 // with draft logits in fp32 (V = 128256): 112 us.  Four CTAs per SM with 64
 // registers against two with 128: 92 to 113 us and 112 to 134, although the
 // leaf alone gains (30 to 26).  Batches loaded ahead of their use cost 10 us
-// (spills); rows of the first child brought to L2 while its parent is summed
-// gain 1 us when greedy and cost 4 to 10 us with sums.
+// (spills).
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -52,6 +51,7 @@ namespace {
 constexpr int kTvThreads = 256;
 constexpr int kTvWarps = kTvThreads / 32;
 constexpr int kTvMaxCluster = 16;
+constexpr int64_t kL2Bytes = 126ll << 20;
 constexpr int kTvCtasPerSm = 4;  // of a large batch; the clusters of a small one have two, with more registers
 
 struct TreeVerifyParams {
@@ -67,6 +67,7 @@ struct TreeVerifyParams {
     int32_t* out_path;
     int32_t N, V, range;  // range: elements per warp, a multiple of a warp's vector step
     int64_t stride;
+    bool ahead;  // rows come from DRAM and there is bandwidth to spare
 };
 
 struct Part {
@@ -488,6 +489,15 @@ __global__ void __launch_bounds__(kTvThreads, kCtasPerSm) tree_verify_kernel(con
         __syncthreads();
         const int nchild = sh.nchild[lv];
         const int32_t *child = sh.child[lv], *ctok = sh.ctok[lv];
+        if (kCtasPerSm == 2 && prm.ahead && nchild > 0) {
+            // the first child is the likeliest to be taken: its rows start on their way to L2
+            const int64_t next = (int64_t(child[0]) - node) * prm.stride * Logit<T>::kSize;
+            const int64_t from = lo * int64_t(Logit<T>::kSize), to = hi * int64_t(Logit<T>::kSize);
+            for (int64_t i = from + lane * 128; i < to; i += 32 * 128) {
+                prefetch_l2(zr + next + i);
+                if (prm.draft) prefetch_l2(yr + next + i);
+            }
+        }
         int acc = -1;
         if constexpr (kGreedy) {
             const Part r = range_argmax<T, kVec>(zr, lo, hi);
@@ -711,6 +721,10 @@ cudaError_t launch(TreeVerifyParams prm, int B, cudaStream_t st) {
                   : set_once<many>(dev, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
+    // Few requests over logits that L2 cannot hold: 12 chains of 39 nodes (V = 146376, fp32, with
+    // draft logits) 268 us with rows brought ahead, 305 without; where L2 holds them it costs 0.5 us
+    // in 13 to 2 in 26, and a large batch has no bandwidth left for it (92 us to 96).
+    prm.ahead = roomy && int64_t(B) * prm.N * prm.stride * Logit<T>::kSize * (prm.draft ? 2 : 1) > kL2Bytes;
     const int step = Batch<T, kVec, 1>::kStep;  // a warp's vector
     const int64_t warps = int64_t(C) * kTvWarps;
     prm.range = static_cast<int>(((prm.V + warps - 1) / warps + step - 1) / step * step);
@@ -740,7 +754,7 @@ extern "C" sv_status sv_tree_verify(const sv_tree_shape* s, const void* target, 
     const bool vec = tree_aligned16(target) && (greedy || tree_aligned16(draft)) && stride * es % 16 == 0;
     TreeVerifyParams prm{target, greedy ? nullptr : draft, tokens, parents, counts, uniforms,
                          greedy ? 1.0 : 1.4426950408889634 / temperature, out_accept_len, out_tokens, out_path,
-                         s->N, s->V, 0, stride};
+                         s->N, s->V, 0, stride, false};
     auto st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (s->dtype == SV_BF16) {

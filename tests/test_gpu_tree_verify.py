@@ -283,6 +283,14 @@ def test_rows_that_are_not_finite_stay_in_bounds(fill, draft, greedy):
         assert bool((tok[b, j + 1:] == -1).all()) and path[b, :j + 1].tolist() == list(range(j + 1))
 
 
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_requests_with_more_logits_than_l2_holds(dtype, draft):
+    N = 70 if dtype == "f32" else 140
+    Case(3, N, 160001, dtype=dtype, draft=draft, width=1, boost=14.0, pad=7, seed=21).check()
+    Case(2, N + 60, 160000, dtype=dtype, draft=draft, width=2, boost=14.0, seed=22).check()
+
+
 def test_no_requests():
     e = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device="cuda")
     n, tok, path = tree.tree_verify(e(0, 3, 9, dt=torch.float32), None, e(0, 3), None, None, e(0, 3, dt=torch.float32))
