@@ -131,9 +131,10 @@ def _call(fn, index, stream, *args):
         raise SpecVerifyError(status, fn.__name__)
 
 
-def _fresh(shape, dtype, device, stream):
-    """A new tensor that may be used on `stream` (None: the current one)."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+def _fresh(like, shape, stream):
+    """A new tensor of the dtype and device of `like` (which the caller checks)
+    that may be used on `stream` (None: the current one)."""
+    t = like.new_empty(shape)
     if stream is not None:
         t.record_stream(stream)   # not given to others before the work there is done
     return t
@@ -155,7 +156,7 @@ def cache_resize(page_table, lens, refcount, page_size, *, status=None, stream=N
     slots, max_pages = _table(page_table)
     dev = _cuda_index("page_table", page_table)
     if status is None:
-        status = _fresh(slots, torch.int32, page_table.device, stream)
+        status = _fresh(page_table, slots, stream)
     pages = refcount.shape
     if len(pages) != 1:
         raise ValueError("refcount must be [pages]")
@@ -177,7 +178,7 @@ def cache_commit(k_cache, v_cache, page_table, lens, path, *, out_lens=None, str
     dev = _cuda_index("page_table", page_table)
     c = _cache(k_cache, v_cache, dev)
     if out_lens is None:
-        out_lens = _fresh(B, torch.int32, page_table.device, stream)
+        out_lens = _fresh(page_table, B, stream)
     if path.dim() != 2:
         raise ValueError("path must be [B, width]")
     width = path.shape[1]
@@ -202,7 +203,7 @@ def cache_fork(k_cache, v_cache, page_table, lens, refcount, src, dst, *, status
         raise ValueError("src must be [forks]")
     n = src.shape[0]
     if status is None:
-        status = _fresh(n, torch.int32, page_table.device, stream)
+        status = _fresh(page_table, n, stream)
     table, stride = _int_rows("page_table", page_table, (slots, max_pages), dev)
     pages = k_cache.shape[-4]
     _call(_library().sv_cache_fork, dev, stream, c, table, stride, slots, max_pages,

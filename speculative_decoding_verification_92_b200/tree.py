@@ -113,12 +113,12 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     token per request is N = 1.  Calls that may run at the same time need
     separate workspaces."""
     if out is None:
-        out = _fresh(q.shape, q.dtype, q.device, stream)
+        out = _fresh(q, q.shape, stream)
     c, shape, ptrs, op, sizes = _attention_shapes(q, k, v, out, k_cache, v_cache, page_table)
     B, N, _, _, D, dev = sizes
     if workspace is None:
         n = max(_workspace_bytes(c, shape, sizes), 256)
-        workspace = _fresh(n, torch.uint8, q.device, stream)
+        workspace = _fresh(q, (n + 1) // 2, stream)   # (two bytes an element)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
     else:
@@ -155,8 +155,7 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
         draft = uniforms = None
     i32, nodes = torch.int32, (B, N)
     if out is None:
-        at = target.device
-        out = _fresh(B, i32, at, stream), _fresh(nodes, i32, at, stream), _fresh(nodes, i32, at, stream)
+        out = _fresh(tokens, B, stream), _fresh(tokens, nodes, stream), _fresh(tokens, nodes, stream)
         outs = [x.data_ptr() for x in out]
     else:
         outs = (_dense("out accept_len", out[0], i32, (B,), dev), _dense("out tokens", out[1], i32, nodes, dev),
