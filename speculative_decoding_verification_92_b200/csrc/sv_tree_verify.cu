@@ -263,7 +263,10 @@ __device__ __forceinline__ Part range_stats(const void* row, int lo, int hi, con
         md = static_cast<double>(ref);
         mc = md * c;
         near = fabs(mc) < 4096.0;
-        least = fmaxf(ref - 900.f / cf, -3.402823466e38f);  // below 2^-900: nothing
+        // Below 2^-900: nothing.  Rounded up, so that a logit is let in only where its exponent is
+        // at least -900: at small temperatures one step of a float below the reference can be
+        // past all that exp2_table holds.
+        least = fmaxf(__fsub_ru(ref, 900.f / cf), -3.402823466e38f);
     };
     refer();
     Sum s[2] = {0, 0};

@@ -295,3 +295,37 @@ def test_no_requests():
     e = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device="cuda")
     n, tok, path = tree.tree_verify(e(0, 3, 9, dt=torch.float32), None, e(0, 3), None, None, e(0, 3, dt=torch.float32))
     assert n.shape == (0,) and tok.shape == path.shape == (0, 3)
+
+
+@pytest.mark.parametrize("T", [1e-9, 2e-9, 5e-9, 2e-8, 1e-7])
+@pytest.mark.parametrize("mode", ["leaf", "ids", "draft"])
+@pytest.mark.parametrize("top", [20.0, 30.0, 100.0, -20.0])
+def test_tiny_temperatures(T, mode, top):
+    """Logits one float apart lie thousands of powers of two apart (or, at the
+    largest T and the smallest logits, a few): a leaf and rejections take the
+    likeliest tokens, whatever stands right below them."""
+    B, N, V = 8, 3, 2000
+    c = Case(B, N, V, draft=mode == "draft", T=T, seed=23, width=2, counts=[1 if mode == "leaf" else N] * B)
+    top = np.float32(top)
+    below = [np.nextafter(top, np.float32(-np.inf))]
+    below.append(np.nextafter(below[0], np.float32(-np.inf)))
+    rng = np.random.default_rng(24)
+    likely = np.array([5, 40, 1300])     # the target's, the first of them where a leaf takes its reference
+    z = rng.choice(np.array([below[0], below[1], top - 1, top - 7], np.float32), (B, N, V))
+    z[..., likely] = top
+    if mode == "draft":                  # the draft's two likely tokens have no probability under the target
+        y = rng.choice(np.array([top - 1, top - 7], np.float32), (B, N, V))
+        y[..., [300, 301]] = top
+        z[..., [300, 301]] = top - 7
+        c.y = torch.from_numpy(y).cuda()
+        c.tokens[:, 1:] = rng.choice([300, 301], (B, N - 1))
+    else:
+        c.tokens[:, 1:] = [300, 7]       # no probability, and (at times) the reference's neighbour
+        z[..., 300] = top - 7
+    c.z = torch.from_numpy(z).cuda()
+    c.u[:, 1:] = np.float32(0.5)
+    c.u[:, 0] = np.linspace(0.02, 0.98, B, dtype=np.float32)
+    want = c.check()
+    assert (want[0] == 0).all()          # (1e-6 and less of the mass is theirs)
+    if T <= 5e-9:
+        assert np.isin(want[1][:, 0], likely).all()
