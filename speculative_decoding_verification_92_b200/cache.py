@@ -131,12 +131,19 @@ def _call(fn, index, stream, *args):
         raise SpecVerifyError(status, fn.__name__)
 
 
-def _fresh(like, shape, stream):
+def _fresh(like, shape, stream, own=False):
     """A new tensor of the dtype and device of `like` (which the caller checks)
-    that may be used on `stream` (None: the current one)."""
-    t = like.new_empty(shape)
-    if stream is not None:
-        t.record_stream(stream)   # not given to others before the work there is done
+    for use on `stream` (None: the current one).  It is taken with that stream
+    current: a block of another stream's memory may still be in use by work
+    that is pending there.  What the caller gets is kept from reuse until the
+    caller's stream is done with it too; `own` memory is used by the call alone."""
+    if stream is None:
+        return like.new_empty(shape)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape)
+    if not own and stream != current:
+        t.record_stream(current)
     return t
 
 

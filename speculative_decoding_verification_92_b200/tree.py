@@ -118,7 +118,7 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
     B, N, _, _, D, dev = sizes
     if workspace is None:
         n = max(_workspace_bytes(c, shape, sizes), 256)
-        workspace = _fresh(q, (n + 1) // 2, stream)   # (two bytes an element)
+        workspace = _fresh(q, (n + 1) // 2, stream, own=True)   # (two bytes an element)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
     else:

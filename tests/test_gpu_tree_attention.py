@@ -316,3 +316,25 @@ def test_a_call_s_own_tensors_on_another_stream():
     side.synchronize()
     for out in outs:
         c.check(out, ref)
+
+
+def test_a_call_on_another_stream_is_not_given_memory_that_the_current_stream_still_writes():
+    """Blocks of exactly the output's and the workspace's size are let go while
+    long work on them is pending on the current stream; the call on the other
+    stream, whose inputs are ready, runs meanwhile."""
+    c = Case([900, 300], [9, 9], 9, page=64, seed=21)
+    ref = c.reference()
+    n = tree.tree_attention_workspace_bytes(c.q, c.k, c.v, c.kc, c.vc, c.table)
+    side = torch.cuda.Stream()
+    c.run(stream=side, out=None)         # all is loaded
+    torch.cuda.synchronize()
+    for _ in range(3):
+        pending = [torch.empty(c.q.shape, dtype=c.dtype, device="cuda"),
+                   torch.empty((n + 1) // 2, dtype=c.dtype, device="cuda")]
+        for _ in range(300):
+            for x in pending:
+                x.fill_(3.0)
+        del x, pending
+        out = c.run(stream=side, out=None)
+        torch.cuda.synchronize()
+        c.check(out, ref)
