@@ -218,8 +218,11 @@ class TreeStep:
         """Takes the pages of this step's trees (``parents [slots, nodes]``,
         ``counts [slots]`` as in ``tree_attention``); returns ``status``."""
         counts = self._full if counts is None else counts
-        if counts.dtype != torch.int32:
-            raise TypeError(f"counts must be {torch.int32}, got {counts.dtype}")
+        index = self.k_cache.get_device()
+        # (before anything of the step's own is written: a captured graph may hold it)
+        if counts.dtype != torch.int32 or counts.shape != self.lens.shape or counts.get_device() != index:
+            _bad_tensor("counts", counts, torch.int32, self.lens.shape, index, "")
+        _dense("parents", parents, torch.int32, (self.lens.shape[0], self.nodes), index)
         torch.clamp(counts, min=0, out=self._want)   # (a count or length that is not valid takes nothing away)
         self._want += self.lens
         torch.where(self.lens < 0, self.lens, self._want, out=self._want)
