@@ -208,7 +208,8 @@ class TreeStep:
         self._want, self._new_lens, self._full = ints(slots), ints(slots), torch.full_like(lens, nodes)
         self._counts, self._trimmed = ints(slots), ints(slots)
         self._verified = ints(slots), ints(slots, nodes), ints(slots, nodes)
-        q, k = (torch.empty(slots, nodes, h, head_dim, dtype=k_cache.dtype, device=dev) for h in (q_heads, heads))
+        row = torch.empty(head_dim, dtype=k_cache.dtype, device=dev)   # (only shapes matter here)
+        q, k = (row.expand(slots, nodes, h, head_dim) for h in (q_heads, heads))
         n = tree_attention_workspace_bytes(q, k, k, k_cache[0], v_cache[0], page_table)
         if n == 0 and slots > 0:
             raise ValueError("no tree attention for a cache of this type, page size or head count")

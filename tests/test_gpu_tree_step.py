@@ -238,3 +238,14 @@ def test_refusals():
         step.attention(0, x[:1], x[:1, :, :2], x[:1, :, :2])
     with pytest.raises(IndexError):
         step.attention(2, x, x[:, :, :2], x[:, :, :2])
+
+
+def test_a_step_takes_no_more_memory_than_it_keeps():
+    k, v, table, lens, ref = state([0] * 64, 4, 8)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    step = tree.TreeStep(k, v, table, lens, ref, 256, 64 * HKV)
+    kept = torch.cuda.memory_allocated() - before
+    assert torch.cuda.max_memory_allocated() - before <= kept + (1 << 20)   # (as many queries alone are 268 MB)
+    assert step.begin().tolist() == [-1] * 64
