@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from speculative_decoding_verification_92_b200 import Status, SpecVerifyError, tree
-from tree_reference import ancestors, attention, attention_tolerance, make_parents
+from tree_reference import ancestors, attention, attention_tolerance, exact_score_tolerance, make_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -338,3 +338,47 @@ def test_a_call_on_another_stream_is_not_given_memory_that_the_current_stream_st
         out = c.run(stream=side, out=None)
         torch.cuda.synchronize()
         c.check(out, ref)
+
+
+class ExactCase(Case):
+    """Queries and keys are whole numbers up to `most` times a power of two each,
+    so that every q.k is exact in 32 bits (and some are equal); so is the scale."""
+
+    def __init__(self, *args, most=8, scale=1.0, q_unit=1.0, k_unit=1.0, **kw):
+        super().__init__(*args, **kw)
+        whole = lambda x: (x.float() * most / 2).round().clamp(-most, most).to(x.dtype)
+        for x, unit in ((self.q, q_unit), (self.k, k_unit), (self.kc, k_unit)):   # (NaN stays)
+            x.copy_(whole(x) * unit)
+        self.scale = scale
+
+    def shift(self, at, q0, k0):
+        """The first component: q0 in every query, k0 in the keys of cached rows `at` on (the new ones with them)."""
+        self.q[..., 0], self.k[..., 0] = q0, k0
+        for b, n in enumerate(self.lens):
+            for t in range(n):
+                self.kc[int(self.table[b, t // self.page]), t % self.page, :, 0] = k0 if t >= at else 0.0
+
+    def reference(self):
+        out, A = attention(self.q, self.k, self.v, self.lens, self.counts, self.parents, self.rows_of, self.scale)
+        vmax = max(float(x.nan_to_num().abs().max()) for x in (self.vc, self.v))
+        return out, exact_score_tolerance(out.nan_to_num(), A.nan_to_num(), self.dtype, max(self.lens) + self.N, vmax)
+
+    def run(self, **kw):
+        return super().run(scale=self.scale, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,g", [(128, 4), (64, 7)])
+@pytest.mark.parametrize("scale", [2.0 ** -6, 2.0 ** -3, -2.0 ** -3, 1.0, 4.0])
+def test_exact_scores_from_flat_to_one_hot(dtype, D, g, scale):
+    # scores up to some thousands; with the larger scales the maximum is nearly everything, and moves all the time
+    c = ExactCase([700, 64, 2900], [6, 3, 5], 6, g=g, D=D, dtype=dtype, scale=scale, page=32, seed=22)
+    out, tol = c.reference()
+    c.check(ref=(out, tol))
+    # the tolerance tells these from the answer
+    c.scale = scale * 17 / 16
+    other = c.reference()[0]
+    for b, m in enumerate(c.counts):
+        assert bool((out[b, :m].abs() > tol[b, :m]).any())
+        if abs(scale) < 1:
+            assert bool(((other - out)[b, :m].abs() > tol[b, :m]).any())

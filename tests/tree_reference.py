@@ -231,3 +231,18 @@ def commit(k, v, table, lens, path):
                 c[:, table[b, d // page], d % page] = c[:, table[b, s // page], s % page]
         out[b] = base + n
     return k, v, out
+
+
+def exact_score_tolerance(out, A, dtype, rows, vmax):
+    """Per element, where products and sums of q.k are exact in 32 bits: half a
+    step for rounding the result and half a step of A for the weights p.  The
+    exponent x = (s - reference) c has an error of at most 3 2^-24 (|x| + 16)
+    (c is rounded twice, the fused operation once; the reference is within 2^16
+    of the largest weight), below 2^-16 for every weight above 2^-100; 2^x one of 1.0e-4
+    (bf16) or 2.8e-6 (fp16); 2^-20 is for running sums and their joining: all
+    of them twice, for the weight and for the sum.  fp16 weights are kept 2^6
+    up and lose 2^-25 each below 2^-14 (next to a sum of at least 2^6)."""
+    half = torch.finfo(dtype).eps / 2
+    exp2 = 1.0e-4 if dtype == torch.bfloat16 else 2.8e-6
+    lost = rows * 2.0 ** -31 * vmax if dtype == torch.float16 else 0.0
+    return (half * out.abs() + (half + 2 * (2.0 ** -16 + exp2 + 2.0 ** -20)) * A + lost) * (1 + 2 * half)
