@@ -63,7 +63,8 @@ typedef struct {
  * query head h reads key/value head h / (q_heads / heads).  Rows
  * i >= counts[b] of out are left as they are.  The cached keys and values of
  * rows t < lens[b] + counts[b] must be finite; rows past them may hold
- * anything.
+ * anything.  Scores are held in 32 bits, which scale q.k log2(e) must not
+ * overflow.
  *
  * Supported: SV_BF16 and SV_F16, head_dim 64 and 128, page_size 16, 32, 64
  * and 128, q_heads a multiple of heads with at most 64 query heads per key

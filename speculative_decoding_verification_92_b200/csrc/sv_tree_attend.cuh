@@ -284,6 +284,30 @@ __device__ __forceinline__ float tile_top(uint32_t addr) {
     return m;
 }
 
+// A reference is its maximum's s c rounded to a float, the weights' exponents
+// s c - ref are not: past kFar (2^22) the two differ by so much (1 at 2^23, 64
+// at 2^29) that weights would leave the type's range.  A warp with such a row
+// looks for the maximum of every tile, takes a reference that is not above it,
+// and puts exponents of at most `most` in the scores' place.  Up to 2^26 the
+// bound changes nothing; past it, it rounds scores by less than two steps of a
+// float of their size.
+constexpr float kFar = 4194304.f;  // 2^22
+constexpr float kFarRoom = 8.f;    // 2^(6 + 8) is in fp16's range
+__device__ __noinline__ void far_exponents(uint32_t addr, float c, float ref, float most) {
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {
+        uint32_t s[32];
+        tmem_load(s, addr + 32 * w);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const float x = fmaf(__uint_as_float(s[k]), c, -ref);
+            s[k] = __float_as_uint(x > most ? most : x);  // (NaN stays)
+        }
+        tmem_store(addr + 32 * w, s);
+    }
+    tmem_wait_st();
+}
+
 // Weights 2^(s c - ref) of the row's 128 scores, packed in pairs; returns
 // their sum (NaN or past kMostSum where the reference is too low for the type
 // to hold them).  The next 32 scores are on their way while 32 are worked on,
@@ -643,15 +667,17 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                     // piece) is the maximum looked for and the reference moved there.
                     uint32_t packed[64];
                     float part = 0.f;
-                    bool fresh = __any_sync(0xffffffffu, m == -INFINITY);  // a row without a reference
+                    // (a row without a reference, -inf, or one whose reference is far)
+                    bool fresh = !__all_sync(0xffffffffu, fabsf(m) < kFar), far = false;
+                    float ce = c, re = m;  // (chosen here and not at the call: 93.6 us for chains against 95.7)
                     for (;;) {
                         if (!fresh) {
-                            // (a row that sees nothing yet: all weights 0)
-                            part = tile_weights<T>(lanes + s_at(t), c, m == -INFINITY ? 0.f : m, packed);
+                            part = tile_weights<T>(lanes + s_at(t), ce, re, packed);
                             // (a sum that is NaN is not mended by another reference)
-                            if (!__any_sync(0xffffffffu, part > kMostSum)) break;
+                            if (!__any_sync(0xffffffffu, part > kMostSum) || far) break;
                         }
-                        const float top = tile_top(lanes + s_at(t)) * c - H::kShift;
+                        // rounded down, so that no reference lies above its maximum
+                        const float top = __fadd_rd(__fmul_rd(tile_top(lanes + s_at(t)), c), -H::kShift);
                         if (!fresh && !__any_sync(0xffffffffu, top > m)) break;
                         const float f = top > m ? ex2_approx(m - top) : 1.f;  // 0 where there was nothing yet
                         if (top > m) m = top;
@@ -667,6 +693,13 @@ tree_attend_kernel(const AttnParams a, const __grid_constant__ CUtensorMap kmap,
                             }
                         }
                         fresh = false;
+                        far = __any_sync(0xffffffffu, m > -INFINITY && fabsf(m) >= kFar);
+                        re = m == -INFINITY ? 0.f : m;  // (a row that sees nothing yet: all weights 0)
+                        if (far) {
+                            far_exponents(lanes + s_at(t), c, re, H::kShift + kFarRoom);
+                            ce = 1.f;
+                            re = 0.f;
+                        }
                     }
                     l += part;
                     tmem_store(lanes + s_at(t), packed);         // over the scores

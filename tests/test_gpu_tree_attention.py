@@ -382,3 +382,28 @@ def test_exact_scores_from_flat_to_one_hot(dtype, D, g, scale):
         assert bool((out[b, :m].abs() > tol[b, :m]).any())
         if abs(scale) < 1:
             assert bool(((other - out)[b, :m].abs() > tol[b, :m]).any())
+
+
+@pytest.mark.parametrize("dtype,q_unit,k_unit,scale", [
+    (torch.bfloat16, 2.0 ** 10, 2.0 ** 10, 0.125), (torch.bfloat16, 2.0 ** 12, 2.0 ** 12, 1.0),
+    (torch.bfloat16, 2.0 ** 20, 2.0 ** 20, -1.0), (torch.bfloat16, 2.0 ** 45, 2.0 ** 45, 0.125),
+    (torch.bfloat16, 2.0 ** -20, 2.0 ** 60, 2.0 ** 60), (torch.float16, 2.0 ** 11, 2.0 ** 11, 0.125),
+    (torch.float16, 2.0 ** 11, 2.0 ** 11, 4.0), (torch.float16, 2.0 ** 11, 2.0 ** 11, -2.0 ** 60)])
+@pytest.mark.parametrize("N,g,lens", [(6, 4, [700, 64, 2900]), (64, 4, [130, 300, 0])])
+def test_scores_past_what_32_bits_hold_to_a_whole_number(dtype, q_unit, k_unit, scale, N, g, lens):
+    """Finite queries and keys whose scores are so large that the step of a
+    32-bit score is worth many powers of two: the largest scores take all, in
+    equal shares."""
+    ExactCase(lens, [N, N - 1, (N + 1) // 2], N, g=g, dtype=dtype, scale=scale, q_unit=q_unit, k_unit=k_unit, page=16,
+              seed=23).check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("k0", [2.0 ** 11, -2.0 ** 11])
+@pytest.mark.parametrize("scale,at", [(0.125, 0), (0.5, 0), (2.0, 0), (2.0, 500), (4.0, 0), (4.0, 300)])
+def test_small_differences_between_large_scores(dtype, k0, scale, at):
+    """Scores 2^23 and up (or down) from nothing, or from cached row `at` on,
+    that differ by a few whole numbers."""
+    c = ExactCase([700, 64, 1900], [6, 3, 5], 6, dtype=dtype, scale=scale, most=1, page=16, seed=24)
+    c.shift(at, 2.0 ** 12, k0)
+    c.check()
