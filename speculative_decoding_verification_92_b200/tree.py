@@ -22,8 +22,7 @@ __all__ = ["tree_attention", "tree_attention_workspace_bytes", "tree_verify", "T
 
 MAX_NODES = 256     # SV_MAX_NODES of the C header
 
-_VP, _I32, _I64, _F32, _F64, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
-                                    ctypes.c_size_t)
+_VP, _I32, _F32, _F64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
 
 
 # sv_tree_shape: B, N, V, dtype, row_stride; sv_tree_attention_shape: B, N,
