@@ -201,7 +201,9 @@ class TreeStep:
         self.page_table, self.lens, self.refcount, self.nodes = page_table, lens, refcount, nodes
         slots, dev = _table(page_table)[0], k_cache.device
         heads, head_dim = k_cache.shape[3:]
-        _dense("lens", lens, torch.int32, (slots,), _cuda_index("k_cache", k_cache))
+        index = _cuda_index("k_cache", k_cache)
+        _dense("lens", lens, torch.int32, (slots,), index)
+        _dense("refcount", refcount, torch.int32, k_cache.shape[1:2], index)   # (its free pages are the cache's)
         ints = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
         self.status, self.counts, self.parents = ints(slots), None, None
         self._want, self._new_lens, self._full = ints(slots), ints(slots), torch.full_like(lens, nodes)

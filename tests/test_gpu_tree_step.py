@@ -249,3 +249,12 @@ def test_a_step_takes_no_more_memory_than_it_keeps():
     kept = torch.cuda.memory_allocated() - before
     assert torch.cuda.max_memory_allocated() - before <= kept + (1 << 20)   # (as many queries alone are 268 MB)
     assert step.begin().tolist() == [-1] * 64
+
+
+def test_a_pool_of_another_size_than_the_cache_is_refused():
+    k, v, table, lens, ref = state([20, 30], 4, 3)
+    for other in (torch.cat([ref, ref]), ref[:-1], ref[None]):
+        with pytest.raises(ValueError):
+            tree.TreeStep(k, v, table, lens, other, 4, 8)
+    with pytest.raises(TypeError):
+        tree.TreeStep(k, v, table, lens, ref.long(), 4, 8)
