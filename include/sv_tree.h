@@ -119,9 +119,12 @@ SV_API sv_status sv_tree_attention(const sv_tree_attention_shape *shape, const s
  *     of the target's row; the last token is that argmax.
  * The last token is the smallest t whose running weight sum exceeds u W (W:
  * all weight); no weight at all falls back to p.  A leaf draws from p.
- * Only rows of nodes on the accepted path are read, and sums are held in 64
- * bits.  A chain of k drafts gives what spec_verify gives with
- * its uniforms moved by one slot.
+ * Only rows of nodes on the accepted path are read.  Sums that a draw or a
+ * residual is made of are held in 64 bits; an acceptance test is settled by
+ * sums in 32 bits where it clears their error bound, else by sums in 64.  A
+ * chain of k drafts follows the rule of spec_verify with its uniforms moved by
+ * one slot; near ties spec_verify, whose sums are in 32 bits, may answer with a
+ * neighbour.
  *
  *   out_accept_len [B]     accepted drafts j
  *   out_tokens     [B][N]  their tokens, the last token at index j, then -1

@@ -108,8 +108,9 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lens, parents=None, co
 
     Returns ``out`` (like q; rows past ``counts[b]`` are left as they were,
     NaN rows mark a request that is not valid).  bfloat16 and float16,
-    head_dim 64 and 128, page_size 16 to 128 (powers of two); a single new
-    token per request is N = 1.  Calls that may run at the same time need
+    head_dim 64 and 128, page_size 16 to 128 (powers of two).  A single new
+    token per request is N = 1; a prompt fills the cache as chains of up to
+    256 nodes, call by call (``parents`` None, ``lens`` growing).  Calls that may run at the same time need
     separate workspaces."""
     if out is None:
         out = _fresh(q, q.shape, stream)
@@ -142,7 +143,8 @@ def tree_verify(target, draft, tokens, parents, counts, uniforms, temperature=1.
     j of accepted drafts; their tokens and the last token at index j, then -1;
     node 0 and the accepted nodes, then -1 (what ``cache_commit`` takes).  A
     request that is not valid gets -1 throughout.  Only rows on the accepted
-    path are read; sums are held in 64 bits."""
+    path are read.  Draws and residuals come from sums in 64 bits; acceptance
+    tests from sums in 32 where these settle them, else in 64."""
     if target.dim() != 3:
         raise ValueError("target logits must be [B, N, row_stride]")
     rows = target.shape

@@ -407,3 +407,36 @@ def test_small_differences_between_large_scores(dtype, k0, scale, at):
     c = ExactCase([700, 64, 1900], [6, 3, 5], 6, dtype=dtype, scale=scale, most=1, page=16, seed=24)
     c.shift(at, 2.0 ** 12, k0)
     c.check()
+
+
+@pytest.mark.parametrize("g,D", [(4, 128), (1, 64)])
+def test_prompts_fill_the_cache_in_chains(g, D):
+    """Prompts of 600, 256 and 17 tokens, 256 a call, give what one look at all
+    earlier tokens gives."""
+    total, N = [600, 256, 17], 256
+    whole = Case([0, 0, 0], [t if t <= N else N for t in total], N, g=g, D=D, page=16, chain=True, seed=25)
+    gen = torch.Generator("cuda").manual_seed(26)
+    rand = lambda h: torch.randn(3, 600, h, D, generator=gen, device="cuda").to(whole.dtype)
+    q, k, v = rand(whole.Hq), rand(whole.Hkv), rand(whole.Hkv)
+    pages = [-(-t // 16) for t in total]
+    table = torch.full((3, max(pages)), -1, dtype=torch.int32, device="cuda")
+    ids = torch.randperm(sum(pages), generator=gen, device="cuda").int()
+    for b in range(3):
+        table[b, :pages[b]] = ids[sum(pages[:b]):sum(pages[:b + 1])]
+    kc, vc = (torch.full((sum(pages), 16, whole.Hkv, D), math.nan, dtype=whole.dtype, device="cuda") for _ in range(2))
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    got = []
+    for at in range(0, 600, N):
+        counts = torch.tensor([min(max(t - at, 0), N) for t in total], dtype=torch.int32, device="cuda")
+        part = lambda x: torch.nn.functional.pad(x[:, at:at + N], (0, 0, 0, 0, 0, max(0, at + N - 600))).contiguous()
+        got.append(tree.tree_attention(part(q), part(k), part(v), kc, vc, table, lens, counts=counts))
+        lens += counts
+    got = torch.cat(got, 1)
+    for b, t in enumerate(total):
+        none = lambda b, n: (k[b, :0], v[b, :0])
+        chain = [list(range(-1, t - 1))]
+        out, A = attention(q[b:b + 1, :t], k[b:b + 1, :t], v[b:b + 1, :t], [0], [t], chain, none, D ** -0.5)
+        tol = attention_tolerance(q[b:b + 1, :t], float(k[b, :t].double().abs().max()), out, A, whole.dtype, D ** -0.5)
+        assert bool(((got[b:b + 1, :t].double() - out).abs() <= tol).all())
+        rows = lambda c: c[table[b, :pages[b]].long()].flatten(0, 1)[:t]
+        assert torch.equal(rows(kc), k[b, :t]) and torch.equal(rows(vc), v[b, :t])
