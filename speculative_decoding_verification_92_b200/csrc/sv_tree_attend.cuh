@@ -29,14 +29,14 @@
 // Bound.  Up to about 256 rows per head the cache's bytes: 64 KiB of K and V
 // per tile take an SM's share of HBM some 1.5 us, the two products of 256
 // rows about 1.1 us.  Measured, whole call: 64 chains of 9 nodes over 2000
-// rows (360 MB, 8 key heads of 128, groups of 4) 93 us, 3.9 TB/s; 16 trees of
-// 64 nodes over 8k to 16k rows (740 MB, 165 GFLOP) 190 us, 3.9 TB/s and 0.87
-// PFLOP/s, 225 us when a long run of them has brought the SM clock down from
-// 1.97 to 1.6 GHz; one token over 500 rows 12.4 us.  By length: 22 to 29 us a
-// call and, for chains, 1.47 us a tile, which is the copy rate (6.4 TB/s over
-// 32000 rows).  Units of 256 rows take 2.29 us a tile: 1510 cycles for a
-// group's weights, 750 until its products start, 1360 for the two of them,
-// which shared memory feeds (8 KiB each, in no less than 64 cycles).
+// rows (360 MB, 8 key heads of 128, groups of 4) 94 us, 3.8 TB/s; 16 trees of
+// 64 nodes over 8k to 16k rows (740 MB, 165 GFLOP) 194 us, 3.8 TB/s and 0.85
+// PFLOP/s at 1.97 GHz, 227 us and 0.73 once the power limit of a long run of
+// them holds the SM clock at 1.48; one token over 500 rows 12.4 us.  By length:
+// 22 to 29 us a call and, for chains, 1.48 us a tile, which is the copy rate
+// (6.3 TB/s over 32000 rows).  Units of 256 rows take 2.3 us a tile: 1510
+// cycles for a group's weights, 750 until its products start, 1360 for the two
+// of them; the tensor pipe is active 1940 cycles a tile, 60 %.
 //
 // What the registers decide.  A softmax thread holds 64 packed weights and 64
 // scores; ten warps leave it 168 registers.  Spills go to L1, and shared
