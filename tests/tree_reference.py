@@ -240,9 +240,10 @@ def exact_score_tolerance(out, A, dtype, rows, vmax):
     (c is rounded twice, the fused operation once; the reference is within 2^16
     of the largest weight), below 2^-16 for every weight above 2^-100; 2^x one of 1.0e-4
     (bf16) or 2.8e-6 (fp16); 2^-20 is for running sums and their joining: all
-    of them twice, for the weight and for the sum.  fp16 weights are kept 2^6
-    up and lose 2^-25 each below 2^-14 (next to a sum of at least 2^6)."""
+    of them twice, for the weight and for the sum.  Smaller weights may be lost,
+    2^-100 of v each, and fp16 weights, which are kept 2^6 up, lose 2^-25 each
+    below 2^-14 (next to a sum of at least 2^6)."""
     half = torch.finfo(dtype).eps / 2
     exp2 = 1.0e-4 if dtype == torch.bfloat16 else 2.8e-6
-    lost = rows * 2.0 ** -31 * vmax if dtype == torch.float16 else 0.0
+    lost = rows * vmax * (2.0 ** -31 if dtype == torch.float16 else 2.0 ** -100)
     return (half * out.abs() + (half + 2 * (2.0 ** -16 + exp2 + 2.0 ** -20)) * A + lost) * (1 + 2 * half)
