@@ -8,8 +8,8 @@
 // O += P V, l += sum p.  The exponents' range leaves room above the reference
 // and a weight's relative error does not depend on it, so the maximum is not
 // followed: only when a tile's weights come to more than 2^15 is a new one
-// looked for and O and l rescaled.  p is rounded to the cache's type for the
-// second product.
+// looked for and O and l rescaled (scores past 2^22: far_exponents).  p is
+// rounded to the cache's type for the second product.
 //
 // Roles (10 warps).  Warps 0-3 and 4-7 are two softmax groups, a thread per
 // row of S (a lane of tensor memory).  Warp 8 loads K and V tiles by TMA, one
